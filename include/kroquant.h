@@ -274,6 +274,88 @@ int adaln_modulate(const uint16_t *h, int64_t M, int64_t d, const float *shift, 
 int mx_gemm(const uint8_t *qa, const uint8_t *sa, int64_t M, const uint8_t *qb, const uint8_t *sb, int64_t N,
             int64_t K, void *out, int out_bf16, void *stream);
 
+/* ---------------- few-row products and the 4-bit cache ------------------ */
+/*
+ * mx_gemv: products of a few bf16 rows with an MXFP4 weight matrix (W4A16),
+ * the linear layers of a single-token step and of the AdaLN modulation (whose
+ * shift and scale rows come from one conditioning row per sample).
+ * out[m, n] = sum_k x[m, k] W[n, k], W [N, K] in mx_gemm's layout (codes qw
+ * [N, K/2], E8M0 scales sw [N, K/32]; a scale byte 0xFF is NaN).  Weights and
+ * activations are exact in the products; sums are fp32; out is float32 [M, N]
+ * (out_bf16 = 0) or bf16 rounded once to nearest even (out_bf16 = 1).
+ *   x       dev, bf16 [M, K], 16-byte aligned, 0 <= M <= KQ_GEMV_MAX_ROWS
+ *           (more rows: quantize x and call mx_gemm)
+ *   qw      dev, 16-byte aligned           sw  dev, any alignment
+ *   out     dev, 4-byte (float32) or 2-byte (bf16) aligned, not overlapping
+ *   K % 32 == 0, K <= 2^20, N <= 2^21.  M == 0 or N == 0 is a no-op.
+ */
+#define KQ_GEMV_MAX_ROWS 64
+int mx_gemv(const uint16_t *x, int64_t M, const uint8_t *qw, const uint8_t *sw, int64_t N, int64_t K, void *out,
+            int out_bf16, void *stream);
+
+/*
+ * A paged key/value cache in MXFP4.  The caller owns its four buffers; a page
+ * holds page_size positions of every head:
+ *   kq, vq  dev, uint8 [pages, heads, page_size, dim/2], 16-byte aligned
+ *   ks, vs  dev, uint8 [pages, heads, dim/32, page_size], 16-byte aligned
+ * (E2M1 codes, element 2i in the low nibble; one E8M0 byte per 32 channels of
+ * a position and head).  dim % 32 == 0, dim <= 256; page_size % 16 == 0,
+ * 16 <= page_size <= 1024; 1 <= heads <= 1024; 1 <= pages <= 2^31 - 1.
+ */
+typedef struct mx_cache {
+    uint8_t *kq, *ks, *vq, *vs;
+    int64_t pages, page_size, heads, dim;
+} mx_cache;
+
+/*
+ * The rows of one step, of several sequences one after the other, and where
+ * the sequences lie in a cache:
+ *   page_table  dev, int32 [seqs, width]: page of positions [i page_size,
+ *               (i + 1) page_size) of each sequence
+ *   row_start   dev, int32 [seqs + 1], not decreasing: rows row_start[i] ..
+ *               row_start[i + 1] - 1 belong to sequence i
+ *   lengths     dev, int32 [seqs]: positions of sequence i, its rows included
+ * Row r of sequence i is position lengths[i] - row_start[i + 1] + r: its rows
+ * are its last positions.  The three arrays are read on the device, 4-byte
+ * aligned, and none of their values can make a kernel leave its buffers: a
+ * sequence whose rows do not lie in order inside [0, rows) has none, and a
+ * position that is negative, past width * page_size, or on a page outside
+ * [0, pages) has no slot.  Rows outside every sequence and rows without a
+ * slot are left as they were (mx_cache_read), dropped (mx_cache_write).
+ * 0 <= rows <= 2^28, 0 <= seqs <= 2^20, 0 <= width, width * page_size <= 2^30.
+ */
+typedef struct mx_batch {
+    const int32_t *page_table, *row_start, *lengths;
+    int64_t seqs, width, rows;
+} mx_batch;
+
+/*
+ * mx_cache_write: quantizes the keys and values of a step's rows into their
+ * slots.  Each 32-channel block of a row is quantized as by mx_quantize_f32;
+ * with `factors` the keys first go through the Kronecker transform, and get
+ * the codes that kq_quantize_ex(KQ_VARIANT_BUTTERFLY) gives k as a matrix
+ * [rows, heads * dim] (scores are then taken with queries transformed by the
+ * transposed inverse; values need none of this online, their transform folds
+ * into the projections on either side).
+ *   k, v      dev, bf16 [rows, heads, dim], 16-byte aligned; rows are
+ *             k_stride / v_stride elements apart (multiples of 8, at least
+ *             heads * dim), so both may be slices of one projection's output
+ *   factors   NULL, or dev, float32 [nT, 5, 2, 2], nT = 1 or heads * dim / 32
+ *   cache, batch  host structs, read during the call
+ * Two rows with the same slot (a page that two sequences share) leave a mix
+ * of the two there.  rows == 0 or seqs == 0 is a no-op.
+ */
+int mx_cache_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride, const float *factors,
+                   int64_t nT, const mx_cache *cache, const mx_batch *batch, void *stream);
+
+/*
+ * mx_cache_read: the positions of a batch's rows back as bf16 (the values the
+ * codes stand for, exactly; a block with scale byte 0xFF is NaN).  A batch
+ * whose row_start counts whole sequences reads them whole.
+ *   k, v  dev, bf16 [rows, heads, dim], 16-byte aligned, dense
+ */
+int mx_cache_read(const mx_cache *cache, const mx_batch *batch, uint16_t *k, uint16_t *v, void *stream);
+
 /* ---------------- host helpers for the offline weight side --------------- */
 /* All pointers are host memory; the calls are synchronous and touch no GPU.  */
 

@@ -6,6 +6,7 @@ GPU and enqueue on the given stream (default: torch's current stream); they
 return without synchronising.  There is no fallback: if the library is not
 built, importing this module raises.
 """
+import collections
 import ctypes
 import os
 
@@ -39,7 +40,10 @@ EXPORTS = (
     "kq_measure_copy41",
     # for callers that cannot allocate
     "kq_adaln_quantize_noalloc",
+    # few-row products and the 4-bit key/value cache
+    "mx_gemv", "mx_cache_write", "mx_cache_read",
 )
+KQ_GEMV_MAX_ROWS = 64
 KQ_NOALLOC_MAX_ROWS = 131072
 KQ_COPY_FORMS = 10
 
@@ -72,6 +76,16 @@ def _tuning(tuning):
     return ctypes.byref(Tuning(**{k: int(v) for k, v in tuning.items()}))
 
 
+class _CacheArg(ctypes.Structure):  # mx_cache in kroquant.h
+    _fields_ = [("kq", _P), ("ks", _P), ("vq", _P), ("vs", _P), ("pages", _I64), ("page_size", _I64),
+                ("heads", _I64), ("dim", _I64)]
+
+
+class _BatchArg(ctypes.Structure):  # mx_batch in kroquant.h
+    _fields_ = [("page_table", _P), ("row_start", _P), ("lengths", _P), ("seqs", _I64), ("width", _I64),
+                ("rows", _I64)]
+
+
 _lib.kq_quantize.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _P]
 _lib.kq_quantize_ex.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _INT, _P]
 _lib.kq_transform_f32.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P]
@@ -89,6 +103,9 @@ _lib.fwht_quantize.argtypes = [_P, _I64, _I64, _P, _P, _P]
 _lib.fwht_transform_f32.argtypes = [_P, _I64, _I64, _P, _P]
 _lib.kq_lu_factors.argtypes = [_P, _I64, _P]
 _lib.mx_gemm.argtypes = [_P, _P, _I64, _P, _P, _I64, _I64, _P, _INT, _P]
+_lib.mx_gemv.argtypes = [_P, _I64, _P, _P, _I64, _I64, _P, _INT, _P]
+_lib.mx_cache_write.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P]
+_lib.mx_cache_read.argtypes = [_P, _P, _P, _P, _P]
 _lib.kq_quantize16.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _P]
 _lib.kq_transform16_f32.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P]
 _lib.kq_adaln_quantize.argtypes = [_P, _I64, _I64, _P, _P, _I64, ctypes.c_float, _P, _I64, _P, _P, _P, _P]
@@ -449,6 +466,139 @@ def measure_copy41(src, dst, form=0, stream=None):
         raise ValueError("dst must hold src.nbytes / 4 bytes")
     _check(_lib.kq_measure_copy41(src.data_ptr(), nbytes, dst.data_ptr(), int(form), _stream_handle(stream)),
            "kq_measure_copy41")
+
+
+# ---------------------------------------------------------------------------
+# few-row products and the 4-bit key/value cache
+# ---------------------------------------------------------------------------
+MXCache = collections.namedtuple("MXCache", "kq ks vq vs")
+MXCache.__doc__ = """The four uint8 buffers of a paged MXFP4 cache: codes kq, vq [pages, heads, page_size, dim/2] and
+scales ks, vs [pages, heads, dim/32, page_size]."""
+
+
+def mx_cache_new(pages, page_size, heads, dim, device="cuda"):
+    """An MXCache of zeros (every position reads as 0)."""
+    torch = _torch()
+    if dim % 32:
+        raise ValueError("dim must be a multiple of 32")
+    q, s = (pages, heads, page_size, dim // 2), (pages, heads, dim // 32, page_size)
+    return MXCache(*(torch.zeros(shape, dtype=torch.uint8, device=device) for shape in (q, s, q, s)))
+
+
+def _call(fn, where, stream, tensors, *args):
+    """fn(*args, stream) with the tensors' device current (they share one)."""
+    torch = _torch()
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t.device != dev:
+            raise ValueError(f"{where}: tensors lie on {dev} and {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream.cuda_stream), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream), where)
+
+
+def _heads_view(t, name, heads, dim):
+    """Address and row stride of a bf16 [rows, heads, dim] view whose rows are
+    dense inside and any 16-byte multiple apart."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a torch tensor on the GPU")
+    if t.dtype not in _bf16_types():
+        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [rows, {heads}, {dim}], is {list(t.shape)}")
+    row, head, one = t.stride()
+    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (row if t.shape[0] > 1 else heads * dim)
+
+
+def _cache_arg(cache):
+    u8 = (_torch().uint8,)
+    if cache.kq.dim() != 4:
+        raise ValueError("cache.kq must be [pages, heads, page_size, dim/2]")
+    pages, heads, size, half = cache.kq.shape
+    scales = (pages, heads, half // 16, size)
+    if cache.vq.shape != cache.kq.shape or tuple(cache.ks.shape) != scales or tuple(cache.vs.shape) != scales:
+        raise ValueError("the cache's buffers do not match: codes [pages, heads, page_size, dim/2], scales "
+                         "[pages, heads, dim/32, page_size]")
+    return _CacheArg(_dev(cache.kq, u8, "cache.kq"), _dev(cache.ks, u8, "cache.ks"), _dev(cache.vq, u8, "cache.vq"),
+                     _dev(cache.vs, u8, "cache.vs"), pages, size, heads, half * 2)
+
+
+def _batch_arg(page_table, row_start, lengths, rows):
+    i32 = (_torch().int32,)
+    seqs = lengths.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != seqs or row_start.numel() != seqs + 1:
+        raise ValueError("a batch is page_table [seqs, width], row_start [seqs + 1], lengths [seqs]")
+    return _BatchArg(_dev(page_table, i32, "page_table"), _dev(row_start, i32, "row_start"),
+                     _dev(lengths, i32, "lengths"), seqs, page_table.shape[1], rows)
+
+
+def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
+    """out = x . W^T of at most KQ_GEMV_MAX_ROWS bf16 rows x [M, K] and an
+    MXFP4 matrix W (codes [N, K/2], scales [N, K/32] u8), summed in fp32; out
+    float32 (the default) or bfloat16 [M, N]."""
+    torch = _torch()
+    M, K = _md(x)
+    if qw.dim() != 2 or sw.dim() != 2 or qw.shape[1] * 2 != K or tuple(sw.shape) != (qw.shape[0], K // 32):
+        raise ValueError("operand shapes do not match")
+    N = qw.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=x.device)
+    if out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (M, N):
+        raise ValueError("out must be float32 or bfloat16 [M, N]")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    u8 = (torch.uint8,)
+    _call(_lib.mx_gemv, "mx_gemv", stream, (x, qw, sw, out), _dev(x, _bf16_types(), "x"), M, _dev(qw, u8, "qw"),
+          _dev(sw, u8, "sw"), N, K, _dev(out, (out.dtype,), "out"), 1 if out.dtype == torch.bfloat16 else 0)
+    return out
+
+
+def mx_cache_write(k, v, cache, page_table, row_start, lengths, factors=None, stream=None):
+    """Quantizes the keys and values [rows, heads, dim] (bf16; row strides are
+    free) of a step into their slots of the cache; `factors` [nT, 5, 2, 2]
+    puts the keys through the Kronecker transform first.  Row r of sequence i
+    is position lengths[i] - row_start[i + 1] + r."""
+    c = _cache_arg(cache)
+    kp, kst = _heads_view(k, "k", c.heads, c.dim)
+    vp, vst = _heads_view(v, "v", c.heads, c.dim)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    b = _batch_arg(page_table, row_start, lengths, k.shape[0])
+    tensors = (k, v, *cache, page_table, row_start, lengths)
+    fp, nT = None, 1
+    if factors is not None:
+        fp, nT = _dev(factors, (_torch().float32,), "factors"), _nT(factors)
+        tensors += (factors,)
+    _call(_lib.mx_cache_write, "mx_cache_write", stream, tensors, kp, kst, vp, vst, fp, nT, ctypes.byref(c),
+          ctypes.byref(b))
+
+
+def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=None, stream=None):
+    """Keys and values (bf16 [rows, heads, dim]) of a batch's rows, as the
+    cache's codes stand for them.  `rows` sizes the outputs allocated here;
+    rows of no sequence, or without a slot, are left as they were."""
+    torch = _torch()
+    c = _cache_arg(cache)
+    if rows is None:
+        if k is None:
+            raise ValueError("give rows, or k and v")
+        rows = k.shape[0]
+    shape = (int(rows), c.heads, c.dim)
+    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device) if t is None else t for t in (k, v))
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    b = _batch_arg(page_table, row_start, lengths, shape[0])
+    _call(_lib.mx_cache_read, "mx_cache_read", stream, (k, v, *cache, page_table, row_start, lengths),
+          ctypes.byref(c), ctypes.byref(b), _dev(k, _bf16_types(), "k"), _dev(v, _bf16_types(), "v"))
+    return k, v
 
 
 # ---------------------------------------------------------------------------

@@ -142,6 +142,85 @@ int check_param(const float *p, int64_t count, const void *x, int64_t xbytes, co
     return KQ_OK;
 }
 
+// A cache's geometry and buffers.  Each factor is bounded; the byte counts then stay below 2^60.
+int check_cache(const mx_cache *c)
+{
+    if (!c || c->pages < 1 || c->heads < 1 || c->dim < 1 || c->page_size < 1)
+        return KQ_ERR_ARG;
+    if (c->dim % 32 != 0 || c->dim > 256 || c->page_size % 16 != 0 || c->page_size > 1024 || c->heads > 1024 ||
+        c->pages > 0x7FFFFFFF)
+        return KQ_ERR_SHAPE;
+    if (!c->kq || !c->ks || !c->vq || !c->vs)
+        return KQ_ERR_ARG;
+    if (!aligned(c->kq, 16) || !aligned(c->ks, 16) || !aligned(c->vq, 16) || !aligned(c->vs, 16))
+        return KQ_ERR_ALIGN;
+    return KQ_OK;
+}
+
+struct Span {
+    const void *p;
+    int64_t n;
+};
+
+// The cache's four buffers.
+void cache_spans(const mx_cache &c, Span s[4])
+{
+    const int64_t values = c.pages * c.page_size * c.heads * c.dim;
+    s[0] = {c.kq, values / 2};
+    s[1] = {c.ks, values / 32};
+    s[2] = {c.vq, values / 2};
+    s[3] = {c.vs, values / 32};
+}
+
+// Sizes of a batch; `empty` when there is nothing to do (its pointers are
+// then not inspected).
+int check_batch(const mx_batch *b, const mx_cache &c, bool &empty)
+{
+    if (!b || b->rows < 0 || b->seqs < 0 || b->width < 0)
+        return KQ_ERR_ARG;
+    if (b->rows > ((int64_t)1 << 28) || b->seqs > ((int64_t)1 << 20) || b->width > ((int64_t)1 << 30) / c.page_size)
+        return KQ_ERR_SHAPE;
+    empty = b->rows == 0 || b->seqs == 0;
+    if (empty)
+        return KQ_OK;
+    if ((!b->page_table && b->width > 0) || !b->row_start || !b->lengths)
+        return KQ_ERR_ARG;
+    if (!aligned(b->page_table, 4) || !aligned(b->row_start, 4) || !aligned(b->lengths, 4))
+        return KQ_ERR_ALIGN;
+    return KQ_OK;
+}
+
+void batch_spans(const mx_batch &b, Span s[3])
+{
+    s[0] = {b.page_table, b.seqs * b.width * 4};
+    s[1] = {b.row_start, (b.seqs + 1) * 4};
+    s[2] = {b.lengths, b.seqs * 4};
+}
+
+// Does an output overlap an input, or another output?
+int check_overlap(const Span *out, int outs, const Span *in, int ins)
+{
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j)
+            if (overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+                return KQ_ERR_OVERLAP;
+        for (int j = i + 1; j < outs; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                return KQ_ERR_OVERLAP;
+    }
+    return KQ_OK;
+}
+
+// Row stride of a bf16 [rows, width] view, in elements: whole 16-byte pieces.
+int check_stride(int64_t stride, int64_t width)
+{
+    if (stride < width || stride > ((int64_t)1 << 31))
+        return KQ_ERR_SHAPE;
+    return stride % 8 != 0 ? KQ_ERR_ALIGN : KQ_OK;
+}
+
+int64_t strided_bytes(int64_t rows, int64_t stride, int64_t width) { return ((rows - 1) * stride + width) * 2; }
+
 } // namespace
 
 extern "C" {
@@ -383,6 +462,82 @@ int mx_gemm(const uint8_t *qa, const uint8_t *sa, int64_t M, const uint8_t *qb, 
             int64_t K, void *out, int out_bf16, void *stream)
 {
     return mx_gemm_tuned(qa, sa, M, qb, sb, N, K, out, out_bf16, nullptr, stream);
+}
+
+int mx_gemv(const uint16_t *x, int64_t M, const uint8_t *qw, const uint8_t *sw, int64_t N, int64_t K, void *out,
+            int out_bf16, void *stream)
+{
+    if (M < 0 || N < 0 || K <= 0 || (out_bf16 != 0 && out_bf16 != 1))
+        return KQ_ERR_ARG;
+    if (K % 32 != 0 || K > kq::kMaxD || N > ((int64_t)1 << 21) || M > KQ_GEMV_MAX_ROWS)
+        return KQ_ERR_SHAPE;
+    if (M == 0 || N == 0)
+        return KQ_OK;
+    if (!x || !qw || !sw || !out)
+        return KQ_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(out, out_bf16 ? 2 : 4))
+        return KQ_ERR_ALIGN;
+    const Span o[1] = {{out, M * N * (out_bf16 ? 2 : 4)}};
+    const Span in[3] = {{x, M * K * 2}, {qw, N * (K / 2)}, {sw, N * (K / 32)}};
+    if (const int st = check_overlap(o, 1, in, 3))
+        return st;
+    return hip_status(kq::launch_mx_gemv(x, M, qw, sw, N, K, out, out_bf16, (hipStream_t)stream));
+}
+
+int mx_cache_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride, const float *factors,
+                   int64_t nT, const mx_cache *cache, const mx_batch *batch, void *stream)
+{
+    int st = check_cache(cache);
+    if (st)
+        return st;
+    bool empty = false;
+    if ((st = check_batch(batch, *cache, empty)))
+        return st;
+    const int64_t width = cache->heads * cache->dim;
+    if (factors && nT != 1 && nT != width / 32)
+        return KQ_ERR_SHAPE;
+    if (empty)
+        return KQ_OK;
+    if (!k || !v)
+        return KQ_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(factors, 4))
+        return KQ_ERR_ALIGN;
+    if ((st = check_stride(k_stride, width)) || (st = check_stride(v_stride, width)))
+        return st;
+    Span out[4], in[6];
+    cache_spans(*cache, out);
+    batch_spans(*batch, in);
+    in[3] = {k, strided_bytes(batch->rows, k_stride, width)};
+    in[4] = {v, strided_bytes(batch->rows, v_stride, width)};
+    in[5] = {factors, factors ? nT * 80 : 0};
+    if ((st = check_overlap(out, 4, in, 6)))
+        return st;
+    return hip_status(
+        kq::launch_cache_write(k, v, k_stride, v_stride, factors, nT, *cache, *batch, (hipStream_t)stream));
+}
+
+int mx_cache_read(const mx_cache *cache, const mx_batch *batch, uint16_t *k, uint16_t *v, void *stream)
+{
+    int st = check_cache(cache);
+    if (st)
+        return st;
+    bool empty = false;
+    if ((st = check_batch(batch, *cache, empty)))
+        return st;
+    if (empty)
+        return KQ_OK;
+    if (!k || !v)
+        return KQ_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return KQ_ERR_ALIGN;
+    const int64_t bytes = batch->rows * cache->heads * cache->dim * 2;
+    Span in[7];
+    const Span out[2] = {{k, bytes}, {v, bytes}};
+    batch_spans(*batch, in);
+    cache_spans(*cache, in + 3);
+    if ((st = check_overlap(out, 2, in, 7)))
+        return st;
+    return hip_status(kq::launch_cache_read(*cache, *batch, k, v, (hipStream_t)stream));
 }
 
 // shape checks of the 16-element-block entry points

@@ -206,7 +206,21 @@ __device__ __forceinline__ unsigned mx_encode_pair(const float (&v)[8], unsigned
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Eight packed FP4 codes -> bf16, times 2^E of the scale operand.  Exact: an
+// E2M1 value has two significant bits, and 2^-128 .. 2^125 x 6 lie inside
+// bf16's range, subnormals included (checked for all codes and scales on the
+// device).  The NaN scale 0xFF gives NaN.
+__device__ __forceinline__ bf16x8 mx_bf16x8(unsigned w, float sc)
+{
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3);
+    return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
 
 // c + a b in double into a fresh register (the accumulating form of the
 // instruction would first copy the addend, which stays live across rows)

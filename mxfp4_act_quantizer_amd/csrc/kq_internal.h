@@ -1,5 +1,6 @@
 // Internal launch interface between the C ABI (kq_capi.hip) and the kernels
-// (kq_kernels.hip, kq_adaln.hip, kq_gemm.hip).  Arguments are already
+// (kq_kernels.hip, kq_adaln.hip, kq_gemm.hip, kq_gemv.hip, kq_cache.hip,
+// kq_attention.hip).  Arguments are already
 // validated when these are called.  Every launcher takes its launch-shape
 // overrides as an argument (kq_tuning from the public header; all fields 0
 // means the automatic choices the product entry points use), so no launch
@@ -64,6 +65,15 @@ hipError_t launch_mx_f32(const float *x, int64_t M, int64_t d, uint8_t *q, uint8
 // (float32, or bf16 when bf16 != 0) = A[M, K] . B[N, K]^T
 hipError_t launch_mx_gemm(const uint8_t *qa, const uint8_t *sa, int64_t M, const uint8_t *qb, const uint8_t *sb,
                           int64_t N, int64_t K, void *out, int bf16, const Tuning &tn, hipStream_t stream);
+// W4A16 product of M <= KQ_GEMV_MAX_ROWS bf16 rows with an MXFP4 matrix
+hipError_t launch_mx_gemv(const uint16_t *x, int64_t M, const uint8_t *qw, const uint8_t *sw, int64_t N, int64_t K,
+                          void *out, int bf16, hipStream_t stream);
+// The paged MXFP4 cache: rows into their slots (factors: NULL or the keys'
+// transform), and back as bf16
+hipError_t launch_cache_write(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
+                              const float *factors, int64_t nT, const mx_cache &c, const mx_batch &b,
+                              hipStream_t stream);
+hipError_t launch_cache_read(const mx_cache &c, const mx_batch &b, uint16_t *k, uint16_t *v, hipStream_t stream);
 // AdaLN front-end: row statistics (mean, 1/sqrt(var + eps), fp64) into the
 // workspace stats [M, 2], then x = LayerNorm(h) (1 + scale[m / T]) +
 // shift[m / T] rounded to bf16 and either (x null) the transform and MXFP4
