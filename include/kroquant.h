@@ -322,6 +322,7 @@ typedef struct mx_cache {
  * position that is negative, past width * page_size, or on a page outside
  * [0, pages) has no slot.  Rows outside every sequence and rows without a
  * slot are left as they were (mx_cache_read), dropped (mx_cache_write).
+ * (If row_start does decrease, rows of any sequence may be treated as outside.)
  * 0 <= rows <= 2^28, 0 <= seqs <= 2^20, 0 <= width, width * page_size <= 2^30.
  */
 typedef struct mx_batch {
@@ -355,6 +356,44 @@ int mx_cache_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64
  *   k, v  dev, bf16 [rows, heads, dim], 16-byte aligned, dense
  */
 int mx_cache_read(const mx_cache *cache, const mx_batch *batch, uint16_t *k, uint16_t *v, void *stream);
+
+/*
+ * mx_cache_attention: attention of a step's rows over the cache, the rows
+ * themselves included (mx_cache_write comes first): one new token of every
+ * sequence, a chunk of a prompt, or any mix of the two.  For row r at
+ * position p and query head h, with key/value head h / (q_heads / heads):
+ *   out[r, h] = sum_j softmax_j(scale q[r, h] . K_j) V_j
+ * over the positions j <= p that have a slot, and with window > 0 only those
+ * with p - j < window or j < sinks (the first `sinks` positions stay
+ * visible).  Cached values are exact, scores and sums are fp32, the softmax
+ * weights are rounded to bf16 before their products with V, and out is
+ * rounded once to bf16.  A row that sees no position is 0 (so is one whose
+ * visible scores are all -infinity); a NaN in q or in a visible key makes
+ * the row and head NaN, a NaN block of a visible value its channels; what a
+ * row does not see does not touch it.  Rows of no sequence are left as they
+ * were.  Results do not depend on other rows of the same call beyond the
+ * order of the sums, and are the same from call to call.
+ *   q          dev, bf16 [rows, q_heads, dim], 16-byte aligned, rows q_stride
+ *              elements apart (a multiple of 8, at least q_heads * dim)
+ *   q_heads    a multiple of heads, at most 4096; rows * q_heads < 2^31
+ *   scale      1e-30 .. 1e30 (usually 1 / sqrt(dim))
+ *   window     0 (none) .. 2^30;  sinks  0 .. 2^30, ignored without a window
+ *   out        dev, bf16, as q with out_stride
+ *   workspace  dev, 16-byte aligned, workspace_bytes of it: at least what
+ *              mx_cache_attention_workspace gives for the same arguments
+ *              (which may be 0: NULL is then allowed); overwritten.  Calls
+ *              that overlap in time need one each.
+ * dim is 64, 128 or 256 here.  One or two launches on `stream`.  rows == 0 or
+ * seqs == 0 is a no-op.
+ */
+int mx_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q_heads, const mx_cache *cache,
+                       const mx_batch *batch, float scale, int64_t window, int64_t sinks, uint16_t *out,
+                       int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace of mx_cache_attention in bytes, from the sizes alone (the
+ * buffers of cache and batch are not read).  Queries the device. */
+int mx_cache_attention_workspace(int64_t q_heads, const mx_cache *cache, const mx_batch *batch, int64_t window,
+                                 int64_t sinks, int64_t *bytes);
 
 /* ---------------- host helpers for the offline weight side --------------- */
 /* All pointers are host memory; the calls are synchronous and touch no GPU.  */

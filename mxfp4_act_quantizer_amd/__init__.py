@@ -20,6 +20,7 @@ _BINDING_NAMES = (
     "fwht_transform_f32", "kq_lu_factors", "mx_gemm", "kq_adaln_quantize", "adaln_modulate",
     "kq_quantize16", "kq_transform16_f32", "kq_adaln_quantize_noalloc", "KQ_NOALLOC_MAX_ROWS",
     "mx_gemv", "KQ_GEMV_MAX_ROWS", "MXCache", "mx_cache_new", "mx_cache_write", "mx_cache_read",
+    "mx_cache_attention", "mx_cache_attention_workspace",
 )
 __all__ = list(_BINDING_NAMES)
 

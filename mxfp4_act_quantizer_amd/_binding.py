@@ -41,7 +41,7 @@ EXPORTS = (
     # for callers that cannot allocate
     "kq_adaln_quantize_noalloc",
     # few-row products and the 4-bit key/value cache
-    "mx_gemv", "mx_cache_write", "mx_cache_read",
+    "mx_gemv", "mx_cache_write", "mx_cache_read", "mx_cache_attention", "mx_cache_attention_workspace",
 )
 KQ_GEMV_MAX_ROWS = 64
 KQ_NOALLOC_MAX_ROWS = 131072
@@ -106,6 +106,8 @@ _lib.mx_gemm.argtypes = [_P, _P, _I64, _P, _P, _I64, _I64, _P, _INT, _P]
 _lib.mx_gemv.argtypes = [_P, _I64, _P, _P, _I64, _I64, _P, _INT, _P]
 _lib.mx_cache_write.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P]
 _lib.mx_cache_read.argtypes = [_P, _P, _P, _P, _P]
+_lib.mx_cache_attention.argtypes = [_P, _I64, _I64, _P, _P, ctypes.c_float, _I64, _I64, _P, _I64, _P, _I64, _P]
+_lib.mx_cache_attention_workspace.argtypes = [_I64, _P, _P, _I64, _I64, _P]
 _lib.kq_quantize16.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _P]
 _lib.kq_transform16_f32.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P]
 _lib.kq_adaln_quantize.argtypes = [_P, _I64, _I64, _P, _P, _I64, ctypes.c_float, _P, _I64, _P, _P, _P, _P]
@@ -160,8 +162,14 @@ def _check(st, where):
 # device entry points (torch tensors on the GPU)
 # ---------------------------------------------------------------------------
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
 
 
 def _stream_handle(stream):
@@ -183,8 +191,14 @@ def _dev(t, dtypes, name):
 
 
 def _bf16_types():
-    torch = _torch()
-    return (torch.bfloat16, torch.int16, torch.uint16)
+    global _bf16_dtypes
+    if _bf16_dtypes is None:
+        torch = _torch()
+        _bf16_dtypes = (torch.bfloat16, torch.int16, torch.uint16)
+    return _bf16_dtypes
+
+
+_bf16_dtypes = None
 
 
 def _outputs(x, M, d, q, s):
@@ -485,22 +499,41 @@ def mx_cache_new(pages, page_size, heads, dim, device="cuda"):
     return MXCache(*(torch.zeros(shape, dtype=torch.uint8, device=device) for shape in (q, s, q, s)))
 
 
+# These calls are short enough on the GPU that the host side counts: the checks
+# below take the tensor's own attributes one at a time, and the raw handle of
+# the current stream rather than a new Stream object.
+def _gpu(t, dtype, name):
+    """Address of a contiguous GPU tensor of the dtype."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, (dtype,), name)
+
+
+def _gpu_bf16(t, name):
+    """Address of a contiguous GPU tensor of bf16 values (or their bits)."""
+    return _gpu(t, t.dtype if t.dtype in _bf16_types() else _torch().bfloat16, name)
+
+
 def _call(fn, where, stream, tensors, *args):
     """fn(*args, stream) with the tensors' device current (they share one)."""
     torch = _torch()
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t.device != dev:
-            raise ValueError(f"{where}: tensors lie on {dev} and {t.device}")
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: tensors lie on cuda:{dev} and {t.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {dev}")
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream.cuda_stream), where)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    else:
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream), where)
+            st = fn(*args, stream)
+    if st:
+        raise KQError(st, where)
 
 
 def _heads_view(t, name, heads, dim):
@@ -513,31 +546,31 @@ def _heads_view(t, name, heads, dim):
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name} must be [rows, {heads}, {dim}], is {list(t.shape)}")
     row, head, one = t.stride()
-    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     return t.data_ptr(), (row if t.shape[0] > 1 else heads * dim)
 
 
 def _cache_arg(cache):
-    u8 = (_torch().uint8,)
-    if cache.kq.dim() != 4:
+    u8 = _torch().uint8
+    kq, ks, vq, vs = cache
+    if kq.dim() != 4:
         raise ValueError("cache.kq must be [pages, heads, page_size, dim/2]")
-    pages, heads, size, half = cache.kq.shape
-    scales = (pages, heads, half // 16, size)
-    if cache.vq.shape != cache.kq.shape or tuple(cache.ks.shape) != scales or tuple(cache.vs.shape) != scales:
+    pages, heads, size, half = kq.shape
+    if vq.shape != kq.shape or ks.shape != vs.shape or ks.shape != (pages, heads, half // 16, size):
         raise ValueError("the cache's buffers do not match: codes [pages, heads, page_size, dim/2], scales "
                          "[pages, heads, dim/32, page_size]")
-    return _CacheArg(_dev(cache.kq, u8, "cache.kq"), _dev(cache.ks, u8, "cache.ks"), _dev(cache.vq, u8, "cache.vq"),
-                     _dev(cache.vs, u8, "cache.vs"), pages, size, heads, half * 2)
+    return _CacheArg(_gpu(kq, u8, "cache.kq"), _gpu(ks, u8, "cache.ks"), _gpu(vq, u8, "cache.vq"),
+                     _gpu(vs, u8, "cache.vs"), pages, size, heads, half * 2)
 
 
 def _batch_arg(page_table, row_start, lengths, rows):
-    i32 = (_torch().int32,)
+    i32 = _torch().int32
     seqs = lengths.numel()
     if page_table.dim() != 2 or page_table.shape[0] != seqs or row_start.numel() != seqs + 1:
         raise ValueError("a batch is page_table [seqs, width], row_start [seqs + 1], lengths [seqs]")
-    return _BatchArg(_dev(page_table, i32, "page_table"), _dev(row_start, i32, "row_start"),
-                     _dev(lengths, i32, "lengths"), seqs, page_table.shape[1], rows)
+    return _BatchArg(_gpu(page_table, i32, "page_table"), _gpu(row_start, i32, "row_start"),
+                     _gpu(lengths, i32, "lengths"), seqs, page_table.shape[1], rows)
 
 
 def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
@@ -546,18 +579,18 @@ def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
     float32 (the default) or bfloat16 [M, N]."""
     torch = _torch()
     M, K = _md(x)
-    if qw.dim() != 2 or sw.dim() != 2 or qw.shape[1] * 2 != K or tuple(sw.shape) != (qw.shape[0], K // 32):
-        raise ValueError("operand shapes do not match")
     N = qw.shape[0]
+    if qw.shape != (N, K // 2) or sw.shape != (N, K // 32):
+        raise ValueError("operand shapes do not match")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=x.device)
-    if out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (M, N):
+    elif out.shape != (M, N):
         raise ValueError("out must be float32 or bfloat16 [M, N]")
-    if out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    u8 = (torch.uint8,)
-    _call(_lib.mx_gemv, "mx_gemv", stream, (x, qw, sw, out), _dev(x, _bf16_types(), "x"), M, _dev(qw, u8, "qw"),
-          _dev(sw, u8, "sw"), N, K, _dev(out, (out.dtype,), "out"), 1 if out.dtype == torch.bfloat16 else 0)
+    if out.dtype not in (torch.float32, torch.bfloat16) or out.dtype is not (out_dtype or out.dtype):
+        raise ValueError(f"out is {out.dtype}: float32 or bfloat16, as out_dtype says")
+    u8 = torch.uint8
+    _call(_lib.mx_gemv, "mx_gemv", stream, (x, qw, sw, out), _gpu_bf16(x, "x"), M, _gpu(qw, u8, "qw"),
+          _gpu(sw, u8, "sw"), N, K, _gpu(out, out.dtype, "out"), 1 if out.dtype is torch.bfloat16 else 0)
     return out
 
 
@@ -575,7 +608,7 @@ def mx_cache_write(k, v, cache, page_table, row_start, lengths, factors=None, st
     tensors = (k, v, *cache, page_table, row_start, lengths)
     fp, nT = None, 1
     if factors is not None:
-        fp, nT = _dev(factors, (_torch().float32,), "factors"), _nT(factors)
+        fp, nT = _gpu(factors, _torch().float32, "factors"), _nT(factors)
         tensors += (factors,)
     _call(_lib.mx_cache_write, "mx_cache_write", stream, tensors, kp, kst, vp, vst, fp, nT, ctypes.byref(c),
           ctypes.byref(b))
@@ -592,13 +625,75 @@ def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=No
             raise ValueError("give rows, or k and v")
         rows = k.shape[0]
     shape = (int(rows), c.heads, c.dim)
-    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device) if t is None else t for t in (k, v))
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device)
+    if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {list(shape)}")
     b = _batch_arg(page_table, row_start, lengths, shape[0])
     _call(_lib.mx_cache_read, "mx_cache_read", stream, (k, v, *cache, page_table, row_start, lengths),
-          ctypes.byref(c), ctypes.byref(b), _dev(k, _bf16_types(), "k"), _dev(v, _bf16_types(), "v"))
+          ctypes.byref(c), ctypes.byref(b), _gpu_bf16(k, "k"), _gpu_bf16(v, "v"))
     return k, v
+
+
+def _attention_bytes(q_heads, c, b, window, sinks):
+    need = _I64()
+    st = _lib.mx_cache_attention_workspace(q_heads, ctypes.byref(c), ctypes.byref(b), window, sinks,
+                                           ctypes.byref(need))
+    if st:
+        raise KQError(st, "mx_cache_attention")
+    return need.value
+
+
+def mx_cache_attention_workspace(rows, q_heads, cache, page_table, row_start, lengths, window=0, sinks=0):
+    """Bytes of workspace that mx_cache_attention asks for (it depends on the
+    sizes only, not on the lengths)."""
+    with _torch().cuda.device(cache.kq.device):
+        return _attention_bytes(int(q_heads), _cache_arg(cache),
+                                _batch_arg(page_table, row_start, lengths, int(rows)), int(window), int(sinks))
+
+
+def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=None, window=0, sinks=0, out=None,
+                       workspace=None, stream=None):
+    """Attention of the new rows q [rows, q_heads, dim] (bf16; the row stride
+    is free) over the cache, which holds their keys and values already:
+    causal, with window > 0 only the last `window` positions and the first
+    `sinks`.  softmax_scale is 1 / sqrt(dim) by default.  Returns out (bf16,
+    allocated here when not given; rows of no sequence are left as they were).
+    `workspace` is a uint8 tensor of mx_cache_attention_workspace bytes
+    (allocated here when not given)."""
+    torch = _torch()
+    c = _cache_arg(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, dim]")
+    rows, heads, _ = q.shape
+    qp, qst = _heads_view(q, "q", heads, c.dim)
+    if out is None:
+        out = torch.empty((rows, heads, c.dim), dtype=torch.bfloat16, device=q.device)
+    elif out.shape[0] != rows:
+        raise ValueError("out must have q's rows")
+    op, ost = _heads_view(out, "out", heads, c.dim)
+    b = _batch_arg(page_table, row_start, lengths, rows)
+    tensors = (q, out, *cache, page_table, row_start, lengths)
+    if workspace is None:
+        # the size goes by the compute units of the current device: the tensors' one
+        if torch.cuda.current_device() == q.get_device():
+            need = _attention_bytes(heads, c, b, window, sinks)
+        else:
+            with torch.cuda.device(q.device):
+                need = _attention_bytes(heads, c, b, window, sinks)
+        wp = 0
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        need = workspace.numel()
+        tensors += (workspace,)
+    if workspace is not None:
+        wp = _gpu(workspace, torch.uint8, "workspace")
+    _call(_lib.mx_cache_attention, "mx_cache_attention", stream, tensors, qp, qst, heads, ctypes.byref(c),
+          ctypes.byref(b), c.dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, ost, wp, need)
+    return out
 
 
 # ---------------------------------------------------------------------------

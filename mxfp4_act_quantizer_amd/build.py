@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkroquant.so")
 SOURCES = ["kq_kernels.hip", "kq_capi.hip", "kq_host.cpp", "kq_measure.hip", "kq_gemm.hip", "kq_adaln.hip",
-           "kq_gemv.hip", "kq_cache.hip"]
+           "kq_gemv.hip", "kq_cache.hip", "kq_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

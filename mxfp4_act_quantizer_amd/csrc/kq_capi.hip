@@ -540,6 +540,72 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *batch, uint16_t *k, uin
     return hip_status(kq::launch_cache_read(*cache, *batch, k, v, (hipStream_t)stream));
 }
 
+// What both attention entry points ask of their sizes.
+static int check_attention(int64_t q_heads, const mx_cache *cache, const mx_batch *batch, int64_t window,
+                           int64_t sinks, bool &empty)
+{
+    int st = check_cache(cache);
+    if (st)
+        return st;
+    if ((st = check_batch(batch, *cache, empty)))
+        return st;
+    if (q_heads < 1 || window < 0 || sinks < 0)
+        return KQ_ERR_ARG;
+    if (q_heads % cache->heads != 0 || q_heads > 4096 || window > ((int64_t)1 << 30) || sinks > ((int64_t)1 << 30) ||
+        batch->rows > 0x7FFFFFFF / q_heads)
+        return KQ_ERR_SHAPE;
+    if (cache->dim != 64 && cache->dim != 128 && cache->dim != 256)
+        return KQ_ERR_SHAPE;
+    return KQ_OK;
+}
+
+int mx_cache_attention_workspace(int64_t q_heads, const mx_cache *cache, const mx_batch *batch, int64_t window,
+                                 int64_t sinks, int64_t *bytes)
+{
+    bool empty = false;
+    const int st = check_attention(q_heads, cache, batch, window, sinks, empty);
+    if (st)
+        return st;
+    if (!bytes)
+        return KQ_ERR_ARG;
+    *bytes = empty ? 0 : kq::attention_workspace(q_heads, *cache, *batch, window, sinks);
+    return KQ_OK;
+}
+
+int mx_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q_heads, const mx_cache *cache,
+                       const mx_batch *batch, float scale, int64_t window, int64_t sinks, uint16_t *out,
+                       int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    bool empty = false;
+    int st = check_attention(q_heads, cache, batch, window, sinks, empty);
+    if (st)
+        return st;
+    if (!(scale >= 1e-30f) || !(scale <= 1e30f) || workspace_bytes < 0)
+        return KQ_ERR_ARG;
+    if (empty)
+        return KQ_OK;
+    if (!q || !out)
+        return KQ_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16))
+        return KQ_ERR_ALIGN;
+    const int64_t width = q_heads * cache->dim;
+    if ((st = check_stride(q_stride, width)) || (st = check_stride(out_stride, width)))
+        return st;
+    Span in[8];
+    batch_spans(*batch, in);
+    cache_spans(*cache, in + 3);
+    in[7] = {q, strided_bytes(batch->rows, q_stride, width)};
+    const Span o[2] = {{out, strided_bytes(batch->rows, out_stride, width)},
+                       {workspace, workspace ? workspace_bytes : 0}};
+    if ((st = check_overlap(o, 2, in, 8)))
+        return st;
+    const int64_t need = kq::attention_workspace(q_heads, *cache, *batch, window, sinks);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return KQ_ERR_ARG;
+    return hip_status(kq::launch_cache_attention(q, q_stride, q_heads, *cache, *batch, scale, window, sinks, out,
+                                                 out_stride, workspace, (hipStream_t)stream));
+}
+
 // shape checks of the 16-element-block entry points
 static int check_md16(int64_t M, int64_t d, int64_t nT)
 {

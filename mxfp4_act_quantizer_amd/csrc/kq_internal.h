@@ -74,6 +74,12 @@ hipError_t launch_cache_write(const uint16_t *k, const uint16_t *v, int64_t k_st
                               const float *factors, int64_t nT, const mx_cache &c, const mx_batch &b,
                               hipStream_t stream);
 hipError_t launch_cache_read(const mx_cache &c, const mx_batch &b, uint16_t *k, uint16_t *v, hipStream_t stream);
+// Attention over the cache: its workspace in bytes, and the launch (one or
+// two kernels; the workspace is not read when its size is 0)
+int64_t attention_workspace(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t window, int64_t sinks);
+hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q_heads, const mx_cache &c,
+                                  const mx_batch &b, float scale, int64_t window, int64_t sinks, uint16_t *out,
+                                  int64_t out_stride, void *workspace, hipStream_t stream);
 // AdaLN front-end: row statistics (mean, 1/sqrt(var + eps), fp64) into the
 // workspace stats [M, 2], then x = LayerNorm(h) (1 + scale[m / T]) +
 // shift[m / T] rounded to bf16 and either (x null) the transform and MXFP4

@@ -1,16 +1,9 @@
 """Plain float64 references of the few-row product, the paged MXFP4 cache and
 the attention over it, with numpy on the host.  Codes are read through the
-oracle (oracle.mx_dequant, oracle.mx_quantize_f32)."""
+oracle (mx_dequant, mx_quantize_f32)."""
 import numpy as np
 
 from oracle import oracle as O
-
-
-def bf16_round(a):
-    """float64 -> the nearest bf16 value (ties to even), as float64."""
-    flat = np.asarray(a, np.float64).reshape(-1)
-    bits = np.array([O.lib().oracle_double_to_bf16(float(v)) for v in flat], np.uint16)
-    return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64).reshape(np.shape(a))
 
 
 def dequant(q, s):
@@ -45,33 +38,37 @@ def slots(page_table, row_start, lengths, rows, pages, page_size):
     return out
 
 
-def cache_values(codes, scales, page, off):
-    """float64 [heads, dim] of one position."""
-    return dequant(codes[page, :, off], scales[page, :, :, off])
+def attention(q, kq, ks, vq, vs, page_table, row_start, lengths, scale, window=0, sinks=0):
+    """(out, room), float64 [rows, q_heads, dim]: the attention of q (float64)
+    over the cache, and how far a kernel may be from it that sums scores and
+    outputs in fp32 and rounds the weights and the result to bf16.  Rows of no
+    sequence are NaN.
 
-
-def attention(q, kq, ks, vq, vs, page_table, row_start, lengths, scale, window, sinks):
-    """float64 [rows, q_heads, dim]; rows of no sequence are NaN.  q is
-    float64 [rows, q_heads, dim].  The scores and sums of one row at a time."""
+    room = 2^-8 |o| (half a step of the result) + A (2^-8 + 2 e + n 2^-22),
+    A = sum_j w_j |v_j|: half a step of each bf16 weight; e the error of a
+    score as an exponent, (dim + 8) 2^-23 scale max_j sum_d |q_d k_jd|, which
+    enters the weight and the sum it is divided by; n fp32 additions of each
+    sum, an exp2 of about one step of 2^-23 among them.  Underflow: a weight
+    below fp32's normal range (2^-126 before the division) may be flushed, and
+    the largest weight, by which the sum is at least bounded, may be scaled to
+    2^-8 only, so each v_j adds at most 2^-118 |v_j|."""
     rows, q_heads, dim = q.shape
     pages, heads, size, _ = kq.shape
     group = q_heads // heads
-    out = np.full(q.shape, np.nan)
+    out, room = np.full(q.shape, np.nan), np.zeros(q.shape)
     for i, length in enumerate(lengths):
         a, e = int(row_start[i]), int(row_start[i + 1])
         if a < 0 or e > rows or e <= a:
             continue
         span = min(max(int(length), 0), page_table.shape[1] * size)
-        where = [(int(page_table[i, p // size]), p % size) for p in range(span)]
-        there = np.array([0 <= pg < pages for pg, _ in where], bool)
-        k = np.zeros((span, heads, dim))
-        v = np.zeros((span, heads, dim))
-        if there.any():
-            pg = np.array([w[0] for w in where])[there]
-            of = np.array([w[1] for w in where])[there]
-            k[there] = dequant(kq[pg, :, of], ks[pg, :, :, of])
-            v[there] = dequant(vq[pg, :, of], vs[pg, :, :, of])
         j = np.arange(span)
+        pg = page_table[i, j // size].astype(np.int64)
+        there = (pg >= 0) & (pg < pages)
+        k, v = np.zeros((span, heads, dim)), np.zeros((span, heads, dim))
+        if there.any():
+            at, of = pg[there], (j % size)[there]
+            k[there] = dequant(kq[at, :, of], ks[at, :, :, of])
+            v[there] = dequant(vq[at, :, of], vs[at, :, :, of])
         for r in range(a, e):
             p = int(length) - e + r
             seen = there & (j <= p)
@@ -81,9 +78,16 @@ def attention(q, kq, ks, vq, vs, page_table, row_start, lengths, scale, window, 
             if not at.size:
                 out[r] = 0.0
                 continue
-            for h in range(q_heads):
-                s = scale * (k[at, h // group] @ q[r, h])
+            for h in range(heads):
+                qs = q[r, h * group:(h + 1) * group]
                 with np.errstate(invalid="ignore"):
-                    w = np.exp(s - s.max())
-                    out[r, h] = (w / w.sum()) @ v[at, h // group]
-    return out
+                    s = scale * (qs @ k[at, h].T)
+                    w = np.exp(s - s.max(1, keepdims=True))
+                    w /= w.sum(1, keepdims=True)
+                    o, big = w @ v[at, h], w @ np.abs(v[at, h])
+                    err = (dim + 8) * 2.0 ** -23 * scale * (np.abs(qs) @ np.abs(k[at, h]).T).max(1, keepdims=True)
+                out[r, h * group:(h + 1) * group] = o
+                room[r, h * group:(h + 1) * group] = (2.0 ** -8 * np.abs(o)
+                                                      + big * (2.0 ** -8 + 2 * err + at.size * 2.0 ** -22)
+                                                      + 2.0 ** -118 * np.abs(v[at, h]).sum(0))
+    return out, room
