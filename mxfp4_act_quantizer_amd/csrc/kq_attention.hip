@@ -68,6 +68,7 @@ struct AttnArgs {
     float scale2; // scale * log2(e)
     int splits;   // most splits of a sequence
     int wanted;   // workgroups that fill the chip
+    unsigned size16, size_magic; // page_size / 16, and floor(2^32 / size16) + 1
     int tiles;    // column tiles: an upper bound over the batch
 };
 
@@ -225,7 +226,7 @@ __device__ __forceinline__ void load_half(const AttnArgs &a, const Half &at, int
 // NB = dim / 32; kNQ tiles of 16 columns per wave; kWQ waves of a workgroup
 // along the columns, kWaves / kWQ along the cache.
 template <int NB, int kNQ, int kWQ>
-__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttnArgs a)
 {
     constexpr int kWK = kWaves / kWQ;
     constexpr int R = 16 * kNQ * kWQ; // columns of a workgroup
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a)
     const int head = id % heads;
     id /= heads;
     const int split = id % a.splits;
-    const int tile = id / a.splits;
+    const int tile = a.tiles - 1 - id / a.splits; // the last rows see most: they start first
     // the tiles of sequence s start at row_start[s] group / R + s, which leaves
     // it at least ceil(columns / R)
     auto first_of = [&](int s) {
@@ -305,20 +306,23 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a)
     }
 
     const int size = (int)a.c.page_size;
+    const int64_t page_codes = (int64_t)heads * size * (dim / 2), page_scales = (int64_t)heads * size * NB;
     const int32_t *table = a.b.page_table + (int64_t)s * a.b.width;
     auto tile_at = [&](int i) { return i < t.sink_tiles ? i : t.first_tile + i - t.sink_tiles; };
     // both halves of tile index i: their places, and whether they have one
     auto place = [&](int i, Half (&at)[2], bool (&there)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int p = tile_at(i) * kTile + 16 * h;
-            const int pg = p / size, off = p - pg * size;
-            int page = p < t.span ? table[pg] : -1;
-            there[h] = page >= 0 && page < a.c.pages;
+            // u / size16 by multiplication: u < 2^26 and size16 <= 64, so the
+            // product's excess over u / size16 2^32 stays below 2^32
+            const unsigned u = (unsigned)(2 * tile_at(i) + h);
+            const unsigned pg = a.size16 == 1 ? u : __umulhi(u, a.size_magic);
+            const unsigned off = 16 * (u - pg * a.size16);
+            int page = (int)(16 * u) < t.span ? table[pg] : -1;
+            there[h] = page >= 0 && page < (int)a.c.pages;
             page = there[h] ? page : 0;
-            const int64_t block = (int64_t)page * heads + head;
-            at[h].codes = (block * size + off) * (dim / 2);
-            at[h].scales = block * NB * size + off;
+            at[h].codes = page * page_codes + (unsigned)(head * size + off) * (dim / 2);
+            at[h].scales = page * page_scales + (unsigned)(head * NB * size + off);
         }
     };
     auto load = [&](int i, RawTile<NB> &r, bool (&there)[2]) {
@@ -634,29 +638,21 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
     Shape s{};
     const int64_t group = q_heads / c.heads, cols = b.rows * group;
     const int64_t mean = (cols + b.seqs - 1) / b.seqs; // columns of a sequence
-    if (mean <= 16) {
-        s.nq = 1;
-        s.wq = 1;
-    } else if (mean <= 64) {
-        s.nq = 2;
-        s.wq = 1;
-    } else {
-        s.nq = 2;
-        s.wq = 4;
-    }
+    s.wq = mean <= 64 ? 1 : kWaves;
+    s.nq = mean <= 16 || c.dim == 256 ? 1 : 2;
     s.R = 16 * s.nq * s.wq;
     s.tiles = (int)(cols / s.R + b.seqs);
-    s.wanted = 4 * device_cus();
+    s.wanted = (s.wq == 1 ? 4 : 2) * device_cus();
     s.splits = 1;
-    if (b.seqs <= kSplitSeqs) {
+    const int64_t groups = (int64_t)s.tiles * c.heads;
+    if (b.seqs <= kSplitSeqs && 2 * groups <= s.wanted) {
         // tiles of the longest sequence the table can hold
         int64_t span = b.width * c.page_size;
         if (window && window + sinks + b.rows < span)
             span = window + sinks + b.rows;
         const int64_t most = (span / kTile + 2 * kWaves) / (2 * kWaves);
-        const int64_t per = (s.wanted + (int64_t)s.tiles * c.heads - 1) / ((int64_t)s.tiles * c.heads);
         // twice the mean: the longer sequences of a mixed batch take more
-        int64_t n = per > 1 ? 2 * per : 1;
+        int64_t n = 2 * (s.wanted / groups);
         n = n < most ? n : most;
         s.splits = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
     }
@@ -670,12 +666,13 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
     if (grid > 0x7FFFFFFF || a.b.rows * a.q_heads > 0x7FFFFFFF)
         return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), w(64 * kWaves);
-    if (s.nq == 1)
-        attention_kernel<NB, 1, 1><<<g, w, 0, stream>>>(a);
-    else if (s.wq == 1)
-        attention_kernel<NB, 2, 1><<<g, w, 0, stream>>>(a);
+    constexpr int kMost = NB == 8 ? 1 : 2; // column tiles a wave has registers for
+    if (s.wq > 1)
+        attention_kernel<NB, kMost, kWaves><<<g, w, 0, stream>>>(a);
+    else if (s.nq > 1)
+        attention_kernel<NB, kMost, 1><<<g, w, 0, stream>>>(a);
     else
-        attention_kernel<NB, 2, 4><<<g, w, 0, stream>>>(a);
+        attention_kernel<NB, 1, 1><<<g, w, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1)
         return e;
@@ -712,6 +709,8 @@ hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     a.splits = s.splits;
     a.wanted = s.wanted;
+    a.size16 = (unsigned)(c.page_size / 16);
+    a.size_magic = (unsigned)(((uint64_t)1 << 32) / a.size16) + 1;
     a.tiles = s.tiles;
     switch (c.dim) {
     case 64: return launch<2>(a, s, stream);
