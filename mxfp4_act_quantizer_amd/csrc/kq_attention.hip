@@ -24,18 +24,17 @@
 //    NB c, 2 NB (c + 1)) of the positions of its k slots, converts them and
 //    regroups pairs of positions; the j-th product covers channels 2 NB c + j.
 //    A lane then holds 8 NB consecutive channels of its column's output.
-// No shared memory and no barrier in the loop: the cache is read as 4-bit
-// codes (17 bytes per 32 values), small enough to be fetched and converted by
-// every wave that needs it.
 //
 // Softmax: one pass, running maximum and sum.  The maximum used for scaling is
 // raised only when a score exceeds it by 2^8 (weights then stay below 2^8,
 // sums far below fp32's range), so most tiles need no reduction across lanes
 // and no rescaling; the sum is kept per lane and reduced once at the end.
 //
-// Few columns: the waves of a workgroup take every kWK-th tile and join
-// through LDS; long sequences are also split over workgroups, whose partial
-// results a second kernel joins.
+// Few columns (attention_few_kernel): the waves of a workgroup take every
+// fourth tile and join through LDS.  Many (attention_many_kernel): every wave
+// has its own columns, and the converted tiles are shared through LDS.  Where
+// workgroups are few, long sequences are also split over them, and a second
+// kernel joins the parts.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -68,7 +67,7 @@ struct AttnArgs {
     float scale2; // scale * log2(e)
     int splits;   // most splits of a sequence
     int wanted;   // workgroups that fill the chip
-    unsigned size16, size_magic; // page_size / 16, and floor(2^32 / size16) + 1
+    unsigned size16, magic, magic_hi; // page_size / 16; the words of floor(2^32 / size16) + 1
     int tiles;    // column tiles: an upper bound over the batch
 };
 
@@ -149,9 +148,9 @@ __device__ __forceinline__ void plan_tile(const AttnArgs &a, int s, int local, i
 __device__ __forceinline__ float max_groups(float v)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    v = vmax(__uint_as_float(r[0]), __uint_as_float(r[1]));
     const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __builtin_fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
+    return vmax(__uint_as_float(t[0]), __uint_as_float(t[1]));
 }
 
 __device__ __forceinline__ float sum_groups(float v)
@@ -167,6 +166,298 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b)
     return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
+// The work of one workgroup.
+struct Place {
+    int head, split, s, local;
+    TilePlan t;
+    int begin, stop; // its share of the plan's cache tiles
+};
+
+// workgroup -> (split, column tile, head), the head fastest: the eight XCDs
+// take workgroups in turn, so a head's cache stays in few L2s.  The last
+// column tiles, whose rows see most, start first.  False: nothing to do.
+__device__ __forceinline__ bool find_work(const AttnArgs &a, int R, int lane, Place &w)
+{
+    const int heads = (int)a.c.heads;
+    int id = (int)blockIdx.x;
+    w.head = id % heads;
+    id /= heads;
+    w.split = id % a.splits;
+    const int tile = a.tiles - 1 - id / a.splits;
+    // the tiles of sequence s start at row_start[s] group / R + s, which leaves
+    // it at least ceil(columns / R)
+    auto first_of = [&](int s) {
+        const int64_t r = a.b.row_start[s];
+        return (r < 0 ? 0 : r) * a.group / R + s;
+    };
+    w.s = wave_search((int)a.b.seqs, tile, lane, first_of);
+    const int64_t local = tile - first_of(w.s);
+    const SeqRows q = seq_rows(a.b, w.s);
+    if (local < 0 || local * R >= (int64_t)q.rows * a.group)
+        return false;
+    w.local = (int)local;
+    plan_tile(a, w.s, w.local, R, lane, w.t);
+    if (w.split >= w.t.splits)
+        return false;
+    w.begin = w.split * w.t.per_split;
+    w.stop = w.begin + w.t.per_split < w.t.n ? w.begin + w.t.per_split : w.t.n;
+    return true;
+}
+
+// A wave's columns: queries, what each column sees, running sums.
+template <int NB, int kNQ>
+struct Columns {
+    bf16x8 Q[kNQ][NB];
+    f32x4 acc[kNQ][2 * NB];
+    float m[kNQ], l[kNQ];     // scaling maximum (log2), and the lane's part of the sum
+    int pos[kNQ], low[kNQ];   // the column sees [low, pos] and the first `sinks`
+    int row[kNQ], qhead[kNQ];
+    bool live[kNQ];           // not a padding column
+    // positions of the wave's first and last column, and one past what it sees
+    int wmin, wmax, whi;
+    bool idle;                // padding columns only
+};
+
+template <int NB, int kNQ>
+__device__ __forceinline__ void load_columns(const AttnArgs &a, const Place &w, int col0, int c, int g,
+                                             Columns<NB, kNQ> &q)
+{
+    const TilePlan &t = w.t;
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        const int col = col0 + n * 16 + c;
+        q.live[n] = col < t.cols;
+        const int at = q.live[n] ? col : 0, i = at / a.group;
+        q.row[n] = t.seq.first + i;
+        q.qhead[n] = w.head * a.group + at - i * a.group;
+        q.pos[n] = q.live[n] ? (int)(t.seq.pos0 + i) : -1;
+        q.low[n] = a.window && q.live[n] ? q.pos[n] - a.window + 1 : -0x7FFFFFFF;
+        const uint16_t *src = a.q + (int64_t)q.row[n] * a.q_stride + q.qhead[n] * (32 * NB) + g * (8 * NB);
+#pragma unroll
+        for (int p = 0; p < NB; ++p) {
+            u32x4 v = *(const u32x4 *)(src + 8 * p);
+            if (!q.live[n])
+                v = (u32x4){0, 0, 0, 0};
+            q.Q[n][p] = __builtin_bit_cast(bf16x8, v);
+        }
+        q.m[n] = -__builtin_inff();
+        q.l[n] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j)
+            q.acc[n][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const int last = (col0 + kNQ * 16 < t.cols ? col0 + kNQ * 16 : t.cols) - 1;
+    q.idle = col0 >= t.cols;
+    q.wmin = (int)(t.seq.pos0 + col0 / a.group);
+    q.wmax = (int)(t.seq.pos0 + last / a.group);
+    q.whi = q.idle || q.wmax < 0 ? 0 : q.wmax + 1 < t.span ? q.wmax + 1 : t.span;
+}
+
+// Does every column of the wave see all of [j0, j0 + 32)?
+template <int NB, int kNQ>
+__device__ __forceinline__ bool sees_all(const AttnArgs &a, const Columns<NB, kNQ> &q, int j0, int span)
+{
+    return j0 + kTile <= q.wmin + 1 && j0 + kTile <= span && !q.idle &&
+           (!a.window || j0 >= q.wmax - a.window + 1 || j0 + kTile <= a.sinks);
+}
+
+// Scores of what a column does not see become -infinity; `seen` gets the
+// positions (k slot 4h + i: position 16h + 4g + i of the tile) that it sees.
+template <int NB, int kNQ>
+__device__ __forceinline__ void mask_scores(const AttnArgs &a, const Columns<NB, kNQ> &q, int j0, int span,
+                                            const bool (&there)[2], int g, f32x4 (&S)[kNQ][2], unsigned (&seen)[kNQ])
+{
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        seen[n] = 0;
+        const int hi = q.pos[n] < span ? q.pos[n] + 1 : span;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int h = k >> 2, j = j0 + 16 * h + 4 * g + (k & 3);
+            const bool see = (int)(j < hi) & ((int)(j >= q.low[n]) | (int)(j < a.sinks)) & (int)there[h];
+            seen[n] |= (unsigned)see << k;
+            S[n][h][k & 3] = see ? S[n][h][k & 3] : -__builtin_inff();
+        }
+    }
+}
+
+// Scores -> bf16 weights as the next product's column operand; raises the
+// running maximum (and rescales) only where a score passes it by 2^kRaise.
+template <int NB, int kNQ>
+__device__ __forceinline__ void weigh(const AttnArgs &a, Columns<NB, kNQ> &q, const f32x4 (&S)[kNQ][2],
+                                      bf16x8 (&P)[kNQ])
+{
+    bool raise = false;
+    float top[kNQ];
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        float x = vmax(vmax(S[n][0][0], S[n][0][1]), S[n][0][2]);
+        x = vmax(vmax(x, S[n][0][3]), S[n][1][0]);
+        x = vmax(vmax(x, S[n][1][1]), vmax(S[n][1][2], S[n][1][3]));
+        top[n] = x * a.scale2; // a NaN raises nothing, and reaches the sums as a weight
+        raise |= top[n] > q.m[n] + kRaise;
+    }
+    if (__builtin_amdgcn_ballot_w64(raise)) {
+#pragma unroll
+        for (int n = 0; n < kNQ; ++n) {
+            const float up = vmax(q.m[n], max_groups(top[n]));
+            const float f = up == q.m[n] ? 1.0f : __builtin_amdgcn_exp2f(q.m[n] - up);
+            q.m[n] = up;
+            q.l[n] *= f;
+#pragma unroll
+            for (int j = 0; j < 2 * NB; ++j)
+                q.acc[n][j] *= f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        const float base = q.m[n] == -__builtin_inff() ? 0.0f : q.m[n];
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            w[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][k >> 2][k & 3], a.scale2, -base));
+        q.l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        const u32x4 pk = {pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+        P[n] = __builtin_bit_cast(bf16x8, pk);
+    }
+}
+
+// Two bits of a slot mask -> bf16 1.0 / 0.0, for the NaN counts.
+__device__ __forceinline__ bf16x8 ones(unsigned bits)
+{
+    u32x4 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        v[k] = ((bits >> (2 * k) & 1u) * 0x3F80u) | ((bits >> (2 * k + 1) & 1u) * 0x3F800000u);
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// A weight of zero does not hide a NaN of V, so a NaN that only some columns
+// see is taken out of the product, and counted per channel row (ind) and
+// column (seen) by one of its own: where the count is not zero the channel
+// becomes NaN.
+__device__ __forceinline__ void spoil(f32x4 &acc, const f32x4 &count)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        acc[e] = count[e] > 0.0f ? __builtin_nanf("") : acc[e];
+}
+
+// Writes a column's result, or its part of it.  The lane's channels are [8 NB
+// g, 8 NB (g + 1)): channel 2 NB e + j of them is acc[j][e].
+template <int NB, int kNQ>
+__device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w, const Columns<NB, kNQ> &q, int g)
+{
+    constexpr int dim = 32 * NB;
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        if (!q.live[n])
+            continue;
+        if (w.t.splits > 1) {
+            const int64_t at = ((int64_t)w.split * a.b.rows + q.row[n]) * a.q_heads + q.qhead[n];
+            if (g == 0)
+                *(f32x2 *)(a.part_ml + at * 2) = (f32x2){q.m[n], q.l[n]};
+            float *o = a.part_o + at * dim + g * (8 * NB);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < 2 * NB; j += 4)
+                    *(f32x4 *)(o + e * 2 * NB + j) =
+                        (f32x4){q.acc[n][j][e], q.acc[n][j + 1][e], q.acc[n][j + 2][e], q.acc[n][j + 3][e]};
+        } else {
+            const float inv = q.l[n] == 0.0f ? 0.0f : 1.0f / q.l[n];
+            uint16_t *o = a.out + (int64_t)q.row[n] * a.out_stride + q.qhead[n] * dim + g * (8 * NB);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < 2 * NB; j += 4)
+                    *(u32x2 *)(o + e * 2 * NB + j) =
+                        (u32x2){pack_bf16(q.acc[n][j][e] * inv, q.acc[n][j + 1][e] * inv),
+                                pack_bf16(q.acc[n][j + 2][e] * inv, q.acc[n][j + 3][e] * inv)};
+        }
+    }
+}
+
+// Walks a sequence's pages in tiles of 32 positions, as one wave takes them:
+// tile indices first, first + step, ... below stop.  Each half of a tile (16
+// positions) lies in one page.  Page numbers are fetched 32 tiles at a time, a
+// half to a lane, one such window ahead, and handed out by lane: a fetch per
+// tile would have to be waited for in the middle of the loop, and with it
+// everything that is in flight.
+struct Pages {
+    const int32_t *table;
+    int span, pages, size, lane;
+    unsigned size16, magic, magic_hi;
+    unsigned page_codes, page_scales;         // bytes of a page
+    const uint8_t *kq, *ks, *vq, *vs;         // of this head in page 0
+    int sink_tiles, skip;                     // tile index -> tile
+    int first, step, stop;
+    int now, next;                            // this lane's page numbers of two windows
+    int at_tile;                              // tiles taken so far
+
+    __device__ __forceinline__ Pages(const AttnArgs &a, const Place &w, int lane_, int first_, int step_)
+        : table(a.b.page_table + (int64_t)w.s * a.b.width), span(w.t.span), pages((int)a.c.pages),
+          size((int)a.c.page_size), lane(lane_), size16(a.size16), magic(a.magic), magic_hi(a.magic_hi),
+          sink_tiles(w.t.sink_tiles), skip(w.t.first_tile - w.t.sink_tiles), first(first_), step(step_), stop(w.stop)
+    {
+        const unsigned head_codes = (unsigned)size * (unsigned)(a.c.dim / 2); // below 2^18; a page below 2^28
+        const unsigned head_scales = (unsigned)size * (unsigned)(a.c.dim / 32);
+        page_codes = (unsigned)a.c.heads * head_codes;
+        page_scales = (unsigned)a.c.heads * head_scales;
+        kq = a.c.kq + w.head * head_codes;
+        vq = a.c.vq + w.head * head_codes;
+        ks = a.c.ks + w.head * head_scales;
+        vs = a.c.vs + w.head * head_scales;
+        at_tile = 0;
+        now = fetch(0);
+        next = fetch(32);
+    }
+
+    __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : i + skip; }
+
+    // u / size16 by multiplication: u < 2^26 and size16 <= 64, so the
+    // product's excess over u / size16 2^32 stays below 2^32
+    __device__ __forceinline__ unsigned page_of(unsigned u) const { return __umulhi(u, magic) + u * magic_hi; }
+
+    // Page number of the lane's half of tiles [from, from + 32) of the walk
+    // (the last tile's past its end), -1 past the table.
+    __device__ __forceinline__ int fetch(int from) const
+    {
+        const int64_t i = first + (int64_t)step * (from + (lane >> 1));
+        const unsigned u = (unsigned)(2 * tile(i < stop ? (int)i : stop - 1) + (lane & 1));
+        return stop > 0 && (int)(16 * u) < span ? table[page_of(u)] : -1;
+    }
+
+    // The halves' page numbers of the next tile of the walk.
+    __device__ __forceinline__ void take(int (&page)[2])
+    {
+        if (at_tile == 32) {
+            now = next;
+            first += 32 * step;
+            next = fetch(32);
+            at_tile = 0;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            page[h] = __builtin_amdgcn_readlane(now, 2 * at_tile + h);
+        ++at_tile;
+    }
+
+    // Byte offsets of a half's codes and scales in the head's arrays (those of
+    // page 0 where it has no page).
+    __device__ __forceinline__ bool at(int i, int h, int page, unsigned half_row, uint64_t &codes,
+                                       uint64_t &scales) const
+    {
+        const unsigned u = (unsigned)(2 * tile(i) + h);
+        const unsigned off = 16 * (u - page_of(u) * size16);
+        const bool there = page >= 0 && page < pages;
+        const unsigned pg = there ? (unsigned)page : 0u;
+        codes = (uint64_t)pg * page_codes + off * half_row;
+        scales = (uint64_t)pg * page_scales + off;
+        return there;
+    }
+};
+
 // Raw codes and scales of one tile, as one lane reads them.
 template <int NB>
 struct RawTile {
@@ -175,178 +466,114 @@ struct RawTile {
     unsigned ks[2][NB == 8 ? 2 : 1];
     unsigned v[8][kVW]; // k slots: positions 4g + i, 16 + 4g + i
     unsigned vs[2];
+    bool there[2];
 };
 
-// Where half a tile (16 positions, always inside one page) lies.
-struct Half {
-    int64_t codes; // byte offset of its codes
-    int64_t scales;
-};
-
+// Codes of position c's channels [8 NB g, 8 NB (g + 1)) and their scales.
 template <int NB>
-__device__ __forceinline__ void load_half(const AttnArgs &a, const Half &at, int h, int c, int g, RawTile<NB> &r)
+__device__ __forceinline__ void load_keys(const Pages &pages, uint64_t codes, uint64_t scales, int c, int g,
+                                          unsigned (&k)[NB], unsigned (&ks)[NB == 8 ? 2 : 1])
 {
-    const int size = (int)a.c.page_size;
-    const uint8_t *kq = a.c.kq + at.codes, *vq = a.c.vq + at.codes;
-    const uint8_t *ks = a.c.ks + at.scales, *vs = a.c.vs + at.scales;
-    const unsigned kc = (unsigned)(c * (NB * 16) + g * (NB * 4));
+    const int size = pages.size;
+    const uint8_t *src = pages.kq + codes + (unsigned)(c * (NB * 16) + g * (NB * 4));
     if constexpr (NB == 2) {
-        const u32x2 w = *(const u32x2 *)(kq + kc);
-        r.k[h][0] = w[0];
-        r.k[h][1] = w[1];
+        const u32x2 w = *(const u32x2 *)src;
+        k[0] = w[0];
+        k[1] = w[1];
     } else {
 #pragma unroll
         for (int i = 0; i < NB / 4; ++i) {
-            const u32x4 w = *(const u32x4 *)(kq + kc + 16 * i);
+            const u32x4 w = *(const u32x4 *)(src + 16 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                r.k[h][4 * i + j] = w[j];
+                k[4 * i + j] = w[j];
         }
     }
-    const int kb = NB == 8 ? 2 * g : NB == 4 ? g : g >> 1;
-    r.ks[h][0] = ks[(unsigned)(kb * size + c)];
+    const int blk = NB == 8 ? 2 * g : NB == 4 ? g : g >> 1;
+    const uint8_t *sc = pages.ks + scales + (unsigned)(blk * size + c);
+    ks[0] = sc[0];
     if constexpr (NB == 8)
-        r.ks[h][1] = ks[(unsigned)((kb + 1) * size + c)];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const unsigned vc = (unsigned)((4 * g + i) * (NB * 16) + c * NB);
-        if constexpr (NB == 2) {
-            r.v[4 * h + i][0] = *(const uint16_t *)(vq + vc);
-        } else if constexpr (NB == 4) {
-            r.v[4 * h + i][0] = *(const unsigned *)(vq + vc);
-        } else {
-            const u32x2 w = *(const u32x2 *)(vq + vc);
-            r.v[4 * h + i][0] = w[0];
-            r.v[4 * h + i][RawTile<NB>::kVW - 1] = w[1];
-        }
-    }
-    r.vs[h] = *(const unsigned *)(vs + (unsigned)((NB * c / 16) * size + 4 * g));
+        ks[1] = sc[size];
 }
 
-// NB = dim / 32; kNQ tiles of 16 columns per wave; kWQ waves of a workgroup
-// along the columns, kWaves / kWQ along the cache.
-template <int NB, int kNQ, int kWQ>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttnArgs a)
+template <int NB>
+__device__ __forceinline__ void load_tile(Pages &pages, int i, int c, int g, RawTile<NB> &r)
 {
-    constexpr int kWK = kWaves / kWQ;
-    constexpr int R = 16 * kNQ * kWQ; // columns of a workgroup
-    constexpr int dim = 32 * NB;
+    int page[2];
+    pages.take(page);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint64_t codes, scales;
+        r.there[h] = pages.at(i, h, page[h], 16 * NB, codes, scales);
+        load_keys<NB>(pages, codes, scales, c, g, r.k[h], r.ks[h]);
+        const uint8_t *v = pages.vq + codes + (unsigned)(4 * g * (NB * 16) + c * NB);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (NB == 2) {
+                r.v[4 * h + k][0] = *(const uint16_t *)(v + k * (NB * 16));
+            } else if constexpr (NB == 4) {
+                r.v[4 * h + k][0] = *(const unsigned *)(v + k * (NB * 16));
+            } else {
+                const u32x2 w = *(const u32x2 *)(v + k * (NB * 16));
+                r.v[4 * h + k][0] = w[0];
+                r.v[4 * h + k][RawTile<NB>::kVW - 1] = w[1];
+            }
+        }
+        r.vs[h] = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
+    }
+}
+
+// Byte b of a dword of codes -> the two channels as packed bf16.
+__device__ __forceinline__ unsigned cvt_byte(unsigned raw, float sc, int b)
+{
+    bf16x2 v;
+    switch (b) { // the byte is part of the instruction
+    case 0: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 0); break;
+    case 1: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 1); break;
+    case 2: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 2); break;
+    default: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 3); break;
+    }
+    return __builtin_bit_cast(unsigned, v);
+}
+
+// (channel 2b, channel 2b + 1) of eight positions -> each channel's eight positions.
+__device__ __forceinline__ void regroup(const unsigned (&w)[8], bf16x8 &even, bf16x8 &odd)
+{
+    u32x4 e, o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        e[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x05040100u);
+        o[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x07060302u);
+    }
+    even = __builtin_bit_cast(bf16x8, e);
+    odd = __builtin_bit_cast(bf16x8, o);
+}
+
+// Few columns (NB = dim / 32; kNQ tiles of 16): every wave has the same
+// columns and takes every kWaves-th cache tile, straight from memory.
+template <int NB, int kNQ>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs a)
+{
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int wq = wave / kWK, wk = wave % kWK;
-
-    // workgroup -> (split, column tile, head), the head fastest: the eight
-    // XCDs take workgroups in turn, so a head's cache stays in few L2s
-    const int heads = (int)a.c.heads;
-    int id = (int)blockIdx.x;
-    const int head = id % heads;
-    id /= heads;
-    const int split = id % a.splits;
-    const int tile = a.tiles - 1 - id / a.splits; // the last rows see most: they start first
-    // the tiles of sequence s start at row_start[s] group / R + s, which leaves
-    // it at least ceil(columns / R)
-    auto first_of = [&](int s) {
-        const int64_t r = a.b.row_start[s];
-        return (r < 0 ? 0 : r) * a.group / R + s;
-    };
-    const int s = wave_search((int)a.b.seqs, tile, lane, first_of);
-    const int64_t local64 = tile - first_of(s);
-    if (local64 < 0 || local64 > ((int64_t)1 << 31) / R)
+    constexpr int R = 16 * kNQ;
+    Place w;
+    if (!find_work(a, R, lane, w))
         return;
-    const int local = (int)local64;
-    TilePlan t;
-    t.seq = seq_rows(a.b, s);
-    if ((int64_t)local * R >= (int64_t)t.seq.rows * a.group)
-        return;
-    plan_tile(a, s, local, R, lane, t);
-    if (split >= t.splits)
-        return;
-    const int begin = split * t.per_split;
-    const int stop = begin + t.per_split < t.n ? begin + t.per_split : t.n;
+    Columns<NB, kNQ> q;
+    load_columns<NB, kNQ>(a, w, w.local * R, c, g, q);
+    int i = w.begin + wave;
+    Pages pages(a, w, lane, i, kWaves);
 
-    // queries, and what each column sees: [low, p] and the first `sinks`
-    bf16x8 Q[kNQ][NB];
-    int pos[kNQ], low[kNQ], row[kNQ], qhead[kNQ];
-    bool live[kNQ];
-#pragma unroll
-    for (int n = 0; n < kNQ; ++n) {
-        const int col = local * R + (wq * kNQ + n) * 16 + c;
-        live[n] = col < t.cols;
-        const int i = (live[n] ? col : 0) / a.group;
-        row[n] = t.seq.first + i;
-        qhead[n] = head * a.group + (live[n] ? col : 0) - i * a.group;
-        pos[n] = live[n] ? (int)(t.seq.pos0 + i) : -1;
-        low[n] = a.window && live[n] ? pos[n] - a.window + 1 : -0x7FFFFFFF;
-        const uint16_t *q = a.q + (int64_t)row[n] * a.q_stride + qhead[n] * dim + g * (8 * NB);
-#pragma unroll
-        for (int i4 = 0; i4 < NB; ++i4) {
-            u32x4 w = *(const u32x4 *)(q + 8 * i4);
-            if (!live[n])
-                w = (u32x4){0, 0, 0, 0};
-            Q[n][i4] = __builtin_bit_cast(bf16x8, w);
-        }
-    }
-    // positions of the wave's own columns, for tiles that need no mask
-    const int wcol0 = local * R + wq * kNQ * 16;
-    const int wcol1 = (wcol0 + kNQ * 16 < t.cols ? wcol0 + kNQ * 16 : t.cols) - 1;
-    const bool idle = wcol0 >= t.cols; // a wave of padding columns only
-    const int wmin = (int)(t.seq.pos0 + wcol0 / a.group);
-    const int wmax = (int)(t.seq.pos0 + wcol1 / a.group);
-    const int whi = idle || wmax < 0 ? 0 : wmax + 1 < t.span ? wmax + 1 : t.span;
-
-    f32x4 acc[kNQ][2 * NB];
-    float m[kNQ], l[kNQ];
-#pragma unroll
-    for (int n = 0; n < kNQ; ++n) {
-        m[n] = -__builtin_inff();
-        l[n] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j)
-            acc[n][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    const int size = (int)a.c.page_size;
-    const int64_t page_codes = (int64_t)heads * size * (dim / 2), page_scales = (int64_t)heads * size * NB;
-    const int32_t *table = a.b.page_table + (int64_t)s * a.b.width;
-    auto tile_at = [&](int i) { return i < t.sink_tiles ? i : t.first_tile + i - t.sink_tiles; };
-    // both halves of tile index i: their places, and whether they have one
-    auto place = [&](int i, Half (&at)[2], bool (&there)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // u / size16 by multiplication: u < 2^26 and size16 <= 64, so the
-            // product's excess over u / size16 2^32 stays below 2^32
-            const unsigned u = (unsigned)(2 * tile_at(i) + h);
-            const unsigned pg = a.size16 == 1 ? u : __umulhi(u, a.size_magic);
-            const unsigned off = 16 * (u - pg * a.size16);
-            int page = (int)(16 * u) < t.span ? table[pg] : -1;
-            there[h] = page >= 0 && page < (int)a.c.pages;
-            page = there[h] ? page : 0;
-            at[h].codes = page * page_codes + (unsigned)(head * size + off) * (dim / 2);
-            at[h].scales = page * page_scales + (unsigned)(head * NB * size + off);
-        }
-    };
-    auto load = [&](int i, RawTile<NB> &r, bool (&there)[2]) {
-        Half at[2];
-        place(i, at, there);
-        load_half<NB>(a, at[0], 0, c, g, r);
-        load_half<NB>(a, at[1], 1, c, g, r);
-    };
-
-    int i = begin + wk;
+    // codes one tile ahead
     RawTile<NB> next;
-    bool there_next[2];
-    if (i < stop)
-        load(i, next, there_next);
-    for (; i < stop; i += kWK) {
+    if (i < w.stop)
+        load_tile<NB>(pages, i, c, g, next);
+    for (; i < w.stop; i += kWaves) {
         RawTile<NB> r = next;
-        const bool there[2] = {there_next[0], there_next[1]};
-        load(i + kWK < stop ? i + kWK : i, next, there_next);
-        const int j0 = tile_at(i) * kTile;
-        if (kWQ > 1 && j0 >= whi)
-            continue; // past this wave's columns (another wave's still see it)
-
-        const bool full = j0 + kTile <= wmin + 1 && j0 + kTile <= t.span && there[0] && there[1] && !idle &&
-                          (!a.window || j0 >= wmax - a.window + 1 || j0 + kTile <= a.sinks);
+        load_tile<NB>(pages, i + kWaves < w.stop ? i + kWaves : w.stop - 1, c, g, next);
+        const int j0 = pages.tile(i) * kTile;
+        const bool full = r.there[0] && r.there[1] && sees_all<NB, kNQ>(a, q, j0, w.t.span);
 
         f32x4 S[kNQ][2];
 #pragma unroll
@@ -359,7 +586,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttnArgs a)
                 const bf16x8 kf = mx_bf16x8(r.k[h][p], scale_operand(r.ks[h][NB == 8 ? p / 4 : 0]));
 #pragma unroll
                 for (int n = 0; n < kNQ; ++n)
-                    S[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, Q[n][p], S[n][h], 0, 0, 0);
+                    S[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q.Q[n][p], S[n][h], 0, 0, 0);
             }
         }
 
@@ -368,212 +595,268 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttnArgs a)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             vsb[k] = (r.vs[k >> 2] >> (8 * (k & 3))) & 0xFFu;
-
-        unsigned nan_slots = 0; // positions of this lane whose V block is NaN, masked tiles only
-        unsigned seen[kNQ];     // positions (bit 4h + i) that the column sees
+        unsigned nan_slots = 0, seen[kNQ];
         if (!full) {
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n) {
-                seen[n] = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int h = k >> 2, j = j0 + 16 * h + 4 * g + (k & 3);
-                    const bool see = j <= pos[n] && j < t.span && (j >= low[n] || j < a.sinks) && there[h];
-                    seen[n] |= (unsigned)see << k;
-                    S[n][h][k & 3] = see ? S[n][h][k & 3] : -__builtin_inff();
-                }
-            }
-            // A weight of zero does not hide a NaN or an infinity of V: what
-            // lies behind the wave's last position (another length, or never
-            // written) is cleared, and a NaN block counts only for columns
-            // that see it (below).
+            mask_scores<NB, kNQ>(a, q, j0, w.t.span, r.there, g, S, seen);
+            // positions that no column sees (past the last one, or never
+            // written) are cleared: a weight of zero would not hide what they
+            // hold.  NaN blocks are cleared too and counted below.
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int h = k >> 2, j = j0 + 16 * h + 4 * g + (k & 3);
-                const bool dead = j >= whi || !there[h];
+                const bool dead = j >= q.whi || !r.there[h];
                 const bool nan = vsb[k] == 0xFFu && !dead;
                 nan_slots |= (unsigned)nan << k;
                 if (dead || nan) {
                     vsb[k] = 127;
 #pragma unroll
-                    for (int w = 0; w < RawTile<NB>::kVW; ++w)
-                        r.v[k][w] = 0;
+                    for (int x = 0; x < RawTile<NB>::kVW; ++x)
+                        r.v[k][x] = 0;
                 }
-            }
-        }
-
-        // scores -> weights
-        bool raise = false;
-        float top[kNQ];
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) {
-            float x = __builtin_fmaxf(S[n][0][0], S[n][0][1]);
-            x = __builtin_fmaxf(x, __builtin_fmaxf(S[n][0][2], S[n][0][3]));
-            x = __builtin_fmaxf(x, __builtin_fmaxf(S[n][1][0], S[n][1][1]));
-            x = __builtin_fmaxf(x, __builtin_fmaxf(S[n][1][2], S[n][1][3]));
-            top[n] = x * a.scale2;
-            raise |= top[n] > m[n] + kRaise;
-        }
-        if (__builtin_amdgcn_ballot_w64(raise)) {
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n) {
-                const float up = __builtin_fmaxf(m[n], max_groups(top[n]));
-                const float f = up == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - up);
-                m[n] = up;
-                l[n] *= f;
-#pragma unroll
-                for (int j = 0; j < 2 * NB; ++j)
-                    acc[n][j] *= f;
             }
         }
         bf16x8 P[kNQ];
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) {
-            const float base = m[n] == -__builtin_inff() ? 0.0f : m[n];
-            float w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                w[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][k >> 2][k & 3], a.scale2, -base));
-                l[n] += w[k];
-            }
-            const u32x4 pk = {pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]),
-                              pack_bf16(w[6], w[7])};
-            P[n] = __builtin_bit_cast(bf16x8, pk);
-        }
-
+        weigh<NB, kNQ>(a, q, S, P);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            unsigned w[8];
+            unsigned v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const unsigned raw = r.v[k][NB == 8 ? b / 4 : 0];
-                const float sc = scale_operand(vsb[k]);
-                bf16x2 v;
-                switch (b & 3) { // the byte is part of the instruction
-                case 0: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 0); break;
-                case 1: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 1); break;
-                case 2: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 2); break;
-                default: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, sc, 3); break;
-                }
-                w[k] = __builtin_bit_cast(unsigned, v);
-            }
-            u32x4 even, odd; // channels 2b and 2b + 1 of the lane's eight positions
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                even[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x05040100u);
-                odd[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x07060302u);
-            }
+            for (int k = 0; k < 8; ++k)
+                v[k] = cvt_byte(r.v[k][NB == 8 ? b / 4 : 0], scale_operand(vsb[k]), b & 3);
+            bf16x8 even, odd;
+            regroup(v, even, odd);
 #pragma unroll
             for (int n = 0; n < kNQ; ++n) {
-                acc[n][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), P[n],
-                                                                        acc[n][2 * b], 0, 0, 0);
-                acc[n][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), P[n],
-                                                                            acc[n][2 * b + 1], 0, 0, 0);
+                q.acc[n][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, P[n], q.acc[n][2 * b], 0, 0, 0);
+                q.acc[n][2 * b + 1] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, P[n], q.acc[n][2 * b + 1], 0, 0, 0);
             }
         }
-
-        // NaN blocks of V that some column of a masked tile may see: count
-        // them per column with one more product (the rows of a lane share
-        // their block), and spoil the channels where the count is not zero.
+        // the channels of a lane share a block, so one count serves them all
         if (!full && __builtin_amdgcn_ballot_w64(nan_slots != 0)) {
-            u32x4 ind;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                ind[k] = ((nan_slots >> (2 * k) & 1u) * 0x3F80u) | ((nan_slots >> (2 * k + 1) & 1u) * 0x3F800000u);
 #pragma unroll
             for (int n = 0; n < kNQ; ++n) {
-                u32x4 see;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    see[k] = ((seen[n] >> (2 * k) & 1u) * 0x3F80u) | ((seen[n] >> (2 * k + 1) & 1u) * 0x3F800000u);
                 const f32x4 count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, ind), __builtin_bit_cast(bf16x8, see),
-                    (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+                    ones(nan_slots), ones(seen[n]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[n][j][e] = count[e] > 0.0f ? __builtin_nanf("") : acc[n][j][e];
+                    spoil(q.acc[n][j], count);
             }
         }
     }
 
-    // sums over the lane groups, then over the waves that shared the tiles
-#pragma unroll
-    for (int n = 0; n < kNQ; ++n)
-        l[n] = sum_groups(l[n]);
-    if constexpr (kWK > 1) {
-        __shared__ float sm[kWaves][kNQ][16], sl[kWaves][kNQ][16];
-        __shared__ f32x4 so[kWaves - 1][kNQ][2 * NB][64];
-        if (g == 0) {
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n) {
-                sm[wave][n][c] = m[n];
-                sl[wave][n][c] = l[n];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) {
-            float up = sm[0][n][c];
-#pragma unroll
-            for (int w = 1; w < kWK; ++w)
-                up = __builtin_fmaxf(up, sm[w][n][c]);
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWK; ++w) {
-                const float mw = sm[w][n][c];
-                sum += sl[w][n][c] * (mw == up ? 1.0f : __builtin_amdgcn_exp2f(mw - up));
-            }
-            const float f = m[n] == up ? 1.0f : __builtin_amdgcn_exp2f(m[n] - up);
-            m[n] = up;
-            l[n] = sum;
-#pragma unroll
-            for (int j = 0; j < 2 * NB; ++j) {
-                acc[n][j] *= f;
-                if (wave)
-                    so[wave - 1][n][j][lane] = acc[n][j];
-            }
-        }
-        __syncthreads();
-        if (wave)
-            return;
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n)
-#pragma unroll
-            for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-                for (int w = 0; w < kWK - 1; ++w)
-                    acc[n][j] += so[w][n][j][lane];
-    }
-
-    // the lane's channels [8 NB g, 8 NB (g + 1)) of column c: channel 2 NB e + j is acc[j][e]
+    // sums over the lane groups, then over the waves
+    __shared__ float sm[kWaves][kNQ][16], sl[kWaves][kNQ][16];
+    __shared__ f32x4 so[kWaves - 1][kNQ][2 * NB][64];
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
-        if (!live[n])
-            continue;
-        if (t.splits > 1) {
-            const int64_t at = ((int64_t)split * a.b.rows + row[n]) * a.q_heads + qhead[n];
-            if (g == 0)
-                *(f32x2 *)(a.part_ml + at * 2) = (f32x2){m[n], l[n]};
-            float *o = a.part_o + at * dim + g * (8 * NB);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int j = 0; j < 2 * NB; j += 4)
-                    *(f32x4 *)(o + e * 2 * NB + j) =
-                        (f32x4){acc[n][j][e], acc[n][j + 1][e], acc[n][j + 2][e], acc[n][j + 3][e]};
-        } else {
-            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-            uint16_t *o = a.out + (int64_t)row[n] * a.out_stride + qhead[n] * dim + g * (8 * NB);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int j = 0; j < 2 * NB; j += 4)
-                    *(u32x2 *)(o + e * 2 * NB + j) = (u32x2){pack_bf16(acc[n][j][e] * inv, acc[n][j + 1][e] * inv),
-                                                             pack_bf16(acc[n][j + 2][e] * inv, acc[n][j + 3][e] * inv)};
+        q.l[n] = sum_groups(q.l[n]);
+        if (g == 0) {
+            sm[wave][n][c] = q.m[n];
+            sl[wave][n][c] = q.l[n];
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n) {
+        float up = sm[0][n][c];
+#pragma unroll
+        for (int x = 1; x < kWaves; ++x)
+            up = __builtin_fmaxf(up, sm[x][n][c]);
+        float sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) {
+            const float mx = sm[x][n][c];
+            sum += sl[x][n][c] * (mx == up ? 1.0f : __builtin_amdgcn_exp2f(mx - up));
+        }
+        const float f = q.m[n] == up ? 1.0f : __builtin_amdgcn_exp2f(q.m[n] - up);
+        q.m[n] = up;
+        q.l[n] = sum;
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) {
+            q.acc[n][j] *= f;
+            if (wave)
+                so[wave - 1][n][j][lane] = q.acc[n][j];
+        }
+    }
+    __syncthreads();
+    if (wave)
+        return;
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n)
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+            for (int x = 0; x < kWaves - 1; ++x)
+                q.acc[n][j] += so[x][n][j][lane];
+    store_columns<NB, kNQ>(a, w, q, g);
+}
+
+// Many columns: the waves have columns of their own and share the cache tiles
+// through LDS, 64 positions at a time in two stages, already converted: each
+// wave converts a quarter, in the order in which the products read it (one
+// 16-byte piece per lane and operand, so neither side has a bank conflict).
+// Per wave and 32 positions that leaves a quarter of the conversions (24 of
+// 96 vector instructions at dim 128) next to its own softmax.
+template <int NB>
+struct __align__(16) WideStage {
+    u32x4 k[4][NB][64];     // 16 positions each
+    u32x4 v[2][2 * NB][64]; // 32 positions each
+    unsigned char nan[2][64]; // per lane: the slots whose V block was NaN (stored as zeros)
+    unsigned flags[2];        // 1 some of nan is set; 2 and 4 the tile's halves have a page
+};
+
+template <int NB, int kNQ>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_many_kernel(AttnArgs a)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    constexpr int R = 16 * kNQ * kWaves;
+    extern __shared__ __align__(16) unsigned char lds[];
+    WideStage<NB> *stage = (WideStage<NB> *)lds;
+    Place w;
+    if (!find_work(a, R, lane, w))
+        return;
+    Columns<NB, kNQ> q;
+    load_columns<NB, kNQ>(a, w, w.local * R + wave * kNQ * 16, c, g, q);
+    const int end = w.t.pmax < 0 ? 0 : w.t.pmax + 1 < w.t.span ? w.t.pmax + 1 : w.t.span; // of all columns
+
+    // This wave's quarter of a stage: tile `wave / 2` of the two, its keys'
+    // half wave % 2, and of its values the channel bytes' half wave % 2.
+    const int mine = wave >> 1, part = wave & 1;
+    unsigned k[NB], ks[NB == 8 ? 2 : 1], v[8], vs[2];
+    bool there[2];
+    Pages pages(a, w, lane, w.begin + mine, 2);
+    auto clamp = [&](int i) { return i < w.stop ? i : w.stop - 1; };
+    auto load = [&](int i) {
+        int page[2];
+        pages.take(page);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint64_t codes, scales;
+            there[h] = pages.at(i, h, page[h], 16 * NB, codes, scales);
+            if (h == part)
+                load_keys<NB>(pages, codes, scales, c, g, k, ks);
+            const uint8_t *src = pages.vq + codes + (unsigned)(4 * g * (NB * 16) + c * NB) + (NB == 8 ? 4 * part : 0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                v[4 * h + x] = NB == 2 ? (unsigned)*(const uint16_t *)(src + x * (NB * 16))
+                                       : *(const unsigned *)(src + x * (NB * 16));
+            vs[h] = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
+        }
+    };
+    auto convert = [&](int i, WideStage<NB> &st) {
+#pragma unroll
+        for (int p = 0; p < NB; ++p)
+            st.k[wave][p][lane] =
+                __builtin_bit_cast(u32x4, mx_bf16x8(k[p], scale_operand(ks[NB == 8 ? p / 4 : 0])));
+        const int j0 = pages.tile(i) * kTile;
+        unsigned vsb[8], slots = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            vsb[x] = (vs[x >> 2] >> (8 * (x & 3))) & 0xFFu;
+            if (NB != 8)
+                v[x] >>= part ? 4 * NB : 0;
+        }
+        // a scale byte 0xFF: its low seven bits carry into the eighth, which is set
+        const unsigned ff = ((((vs[0] & 0x7F7F7F7Fu) + 0x01010101u) & vs[0]) | (((vs[1] & 0x7F7F7F7Fu) + 0x01010101u) & vs[1])) & 0x80808080u;
+        const bool odd_tile = j0 + kTile > end || !there[0] || !there[1];
+        if (odd_tile || __builtin_amdgcn_ballot_w64(ff != 0)) {
+            // cleared: positions that no column sees, as in
+            // attention_few_kernel, and NaN blocks, which are noted
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int h = x >> 2;
+                const bool dead = j0 + 16 * h + 4 * g + (x & 3) >= end || !there[h], nan = vsb[x] == 0xFFu;
+                slots |= (unsigned)(nan && !dead) << x;
+                vsb[x] = dead || nan ? 127 : vsb[x];
+                v[x] = dead || nan ? 0 : v[x];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) {
+            unsigned x[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                x[y] = cvt_byte(v[y], scale_operand(vsb[y]), b);
+            bf16x8 even, odd;
+            regroup(x, even, odd);
+            st.v[mine][part * NB + 2 * b][lane] = __builtin_bit_cast(u32x4, even);
+            st.v[mine][part * NB + 2 * b + 1][lane] = __builtin_bit_cast(u32x4, odd);
+        }
+        if (part == 0) { // both of the tile's waves know this
+            const bool any = __builtin_amdgcn_ballot_w64(slots != 0) != 0;
+            st.nan[mine][lane] = (unsigned char)slots;
+            if (lane == 0)
+                st.flags[mine] = (unsigned)any | (unsigned)there[0] << 1 | (unsigned)there[1] << 2;
+        }
+    };
+
+    int i = w.begin;
+    if (i < w.stop) {
+        load(clamp(i + mine));
+        convert(clamp(i + mine), stage[0]);
+        load(clamp(i + 2 + mine));
+    }
+    for (int buf = 0; i < w.stop; i += 2, buf ^= 1) {
+        // stage[buf] is written, and every wave is done with the other one
+        __syncthreads();
+        if (i + 2 < w.stop) {
+            convert(clamp(i + 2 + mine), stage[buf ^ 1]);
+            load(clamp(i + 4 + mine));
+        }
+        const WideStage<NB> &st = stage[buf];
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+            const int j0 = pages.tile(i + u) * kTile;
+            if (i + u >= w.stop || j0 >= q.whi)
+                continue;
+            const unsigned flags = (unsigned)__builtin_amdgcn_readfirstlane((int)st.flags[u]);
+            const bool has[2] = {(flags & 2u) != 0, (flags & 4u) != 0};
+            const bool full = has[0] && has[1] && sees_all<NB, kNQ>(a, q, j0, w.t.span);
+            f32x4 S[kNQ][2];
+#pragma unroll
+            for (int n = 0; n < kNQ; ++n)
+                S[n][0] = S[n][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int p = 0; p < NB; ++p) {
+                    const bf16x8 kf = __builtin_bit_cast(bf16x8, st.k[2 * u + h][p][lane]);
+#pragma unroll
+                    for (int n = 0; n < kNQ; ++n)
+                        S[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q.Q[n][p], S[n][h], 0, 0, 0);
+                }
+            }
+            unsigned seen[kNQ];
+            if (!full)
+                mask_scores<NB, kNQ>(a, q, j0, w.t.span, has, g, S, seen);
+            bf16x8 P[kNQ];
+            weigh<NB, kNQ>(a, q, S, P);
+#pragma unroll
+            for (int j = 0; j < 2 * NB; ++j) {
+                const bf16x8 vf = __builtin_bit_cast(bf16x8, st.v[u][j][lane]);
+#pragma unroll
+                for (int n = 0; n < kNQ; ++n)
+                    q.acc[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, P[n], q.acc[n][j], 0, 0, 0);
+            }
+            if (flags & 1u) {
+                const unsigned slots = st.nan[u][lane];
+#pragma unroll
+                for (int n = 0; n < kNQ; ++n) {
+                    const f32x4 count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        ones(slots), ones(full ? 0xFFu : seen[n]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 2 * NB; ++j)
+                        spoil(q.acc[n][j], count);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kNQ; ++n)
+        q.l[n] = sum_groups(q.l[n]);
+    store_columns<NB, kNQ>(a, w, q, g);
 }
 
 // Joins the splits of one row and head: a workgroup of 256 threads, dim / 4
@@ -629,7 +912,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R)
 
 // Columns of a workgroup, and how its waves share them.
 struct Shape {
-    int nq, wq, R;
+    bool many;
+    int nq, R;
     int tiles, splits, wanted;
 };
 
@@ -638,11 +922,11 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
     Shape s{};
     const int64_t group = q_heads / c.heads, cols = b.rows * group;
     const int64_t mean = (cols + b.seqs - 1) / b.seqs; // columns of a sequence
-    s.wq = mean <= 64 ? 1 : kWaves;
+    s.many = mean > 64;
     s.nq = mean <= 16 || c.dim == 256 ? 1 : 2;
-    s.R = 16 * s.nq * s.wq;
+    s.R = 16 * s.nq * (s.many ? kWaves : 1);
     s.tiles = (int)(cols / s.R + b.seqs);
-    s.wanted = (s.wq == 1 ? 4 : 2) * device_cus();
+    s.wanted = (s.many ? 2 : 4) * device_cus();
     s.splits = 1;
     const int64_t groups = (int64_t)s.tiles * c.heads;
     if (b.seqs <= kSplitSeqs && 2 * groups <= s.wanted) {
@@ -667,12 +951,18 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
         return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), w(64 * kWaves);
     constexpr int kMost = NB == 8 ? 1 : 2; // column tiles a wave has registers for
-    if (s.wq > 1)
-        attention_kernel<NB, kMost, kWaves><<<g, w, 0, stream>>>(a);
-    else if (s.nq > 1)
-        attention_kernel<NB, kMost, 1><<<g, w, 0, stream>>>(a);
-    else
-        attention_kernel<NB, 1, 1><<<g, w, 0, stream>>>(a);
+    if (s.many) {
+        constexpr int bytes = 2 * (int)sizeof(WideStage<NB>);
+        const void *fn = (const void *)attention_many_kernel<NB, kMost>;
+        const hipError_t e = allow_dynamic_lds(fn, bytes);
+        if (e != hipSuccess)
+            return e;
+        attention_many_kernel<NB, kMost><<<g, w, bytes, stream>>>(a);
+    } else if (s.nq > 1) {
+        attention_few_kernel<NB, kMost><<<g, w, 0, stream>>>(a);
+    } else {
+        attention_few_kernel<NB, 1><<<g, w, 0, stream>>>(a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1)
         return e;
@@ -710,7 +1000,9 @@ hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q
     a.splits = s.splits;
     a.wanted = s.wanted;
     a.size16 = (unsigned)(c.page_size / 16);
-    a.size_magic = (unsigned)(((uint64_t)1 << 32) / a.size16) + 1;
+    const uint64_t magic = ((uint64_t)1 << 32) / a.size16 + 1;
+    a.magic = (unsigned)magic;
+    a.magic_hi = (unsigned)(magic >> 32);
     a.tiles = s.tiles;
     switch (c.dim) {
     case 64: return launch<2>(a, s, stream);
