@@ -379,26 +379,29 @@ __device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w,
 }
 
 // Walks a sequence's pages in tiles of 32 positions, as one wave takes them:
-// tile indices first, first + step, ... below stop.  Each half of a tile (16
-// positions) lies in one page.  Page numbers are fetched 32 tiles at a time, a
-// half to a lane, one such window ahead, and handed out by lane: a fetch per
-// tile would have to be waited for in the middle of the loop, and with it
-// everything that is in flight.
+// tile indices first, first + step, ... below stop, both halves of a tile
+// (kHalves = 2) or only half `part`.  A half (16 positions) lies in one page.
+// Page numbers are fetched 64 halves at a time, one to a lane, one such window
+// ahead, and handed out by lane: a fetch per tile would have to be waited for
+// in the middle of the loop, and with it everything that is in flight.
+template <int kHalves>
 struct Pages {
+    static constexpr int kWindow = 64 / kHalves; // tiles
     const int32_t *table;
     int span, pages, size, lane;
     unsigned size16, magic, magic_hi;
     unsigned page_codes, page_scales;         // bytes of a page
     const uint8_t *kq, *ks, *vq, *vs;         // of this head in page 0
     int sink_tiles, skip;                     // tile index -> tile
-    int first, step, stop;
+    int first, step, stop, part;
     int now, next;                            // this lane's page numbers of two windows
     int at_tile;                              // tiles taken so far
 
-    __device__ __forceinline__ Pages(const AttnArgs &a, const Place &w, int lane_, int first_, int step_)
+    __device__ __forceinline__ Pages(const AttnArgs &a, const Place &w, int lane_, int first_, int step_, int part_)
         : table(a.b.page_table + (int64_t)w.s * a.b.width), span(w.t.span), pages((int)a.c.pages),
           size((int)a.c.page_size), lane(lane_), size16(a.size16), magic(a.magic), magic_hi(a.magic_hi),
-          sink_tiles(w.t.sink_tiles), skip(w.t.first_tile - w.t.sink_tiles), first(first_), step(step_), stop(w.stop)
+          sink_tiles(w.t.sink_tiles), skip(w.t.first_tile - w.t.sink_tiles), first(first_), step(step_), stop(w.stop),
+          part(part_)
     {
         const unsigned head_codes = (unsigned)size * (unsigned)(a.c.dim / 2); // below 2^18; a page below 2^28
         const unsigned head_scales = (unsigned)size * (unsigned)(a.c.dim / 32);
@@ -410,7 +413,7 @@ struct Pages {
         vs = a.c.vs + w.head * head_scales;
         at_tile = 0;
         now = fetch(0);
-        next = fetch(32);
+        next = fetch(kWindow);
     }
 
     __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : i + skip; }
@@ -419,27 +422,27 @@ struct Pages {
     // product's excess over u / size16 2^32 stays below 2^32
     __device__ __forceinline__ unsigned page_of(unsigned u) const { return __umulhi(u, magic) + u * magic_hi; }
 
-    // Page number of the lane's half of tiles [from, from + 32) of the walk
+    // Page number of the lane's half in the window of the walk that starts at tile `from`
     // (the last tile's past its end), -1 past the table.
     __device__ __forceinline__ int fetch(int from) const
     {
-        const int64_t i = first + (int64_t)step * (from + (lane >> 1));
-        const unsigned u = (unsigned)(2 * tile(i < stop ? (int)i : stop - 1) + (lane & 1));
+        const int64_t i = first + (int64_t)step * (from + lane / kHalves);
+        const unsigned u = (unsigned)(2 * tile(i < stop ? (int)i : stop - 1) + (kHalves == 2 ? lane & 1 : part));
         return stop > 0 && (int)(16 * u) < span ? table[page_of(u)] : -1;
     }
 
-    // The halves' page numbers of the next tile of the walk.
-    __device__ __forceinline__ void take(int (&page)[2])
+    // The page numbers of the next tile of the walk.
+    __device__ __forceinline__ void take(int (&page)[kHalves])
     {
-        if (at_tile == 32) {
+        if (at_tile == kWindow) {
             now = next;
-            first += 32 * step;
-            next = fetch(32);
+            first += kWindow * step;
+            next = fetch(kWindow);
             at_tile = 0;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            page[h] = __builtin_amdgcn_readlane(now, 2 * at_tile + h);
+        for (int h = 0; h < kHalves; ++h)
+            page[h] = __builtin_amdgcn_readlane(now, kHalves * at_tile + h);
         ++at_tile;
     }
 
@@ -470,8 +473,8 @@ struct RawTile {
 };
 
 // Codes of position c's channels [8 NB g, 8 NB (g + 1)) and their scales.
-template <int NB>
-__device__ __forceinline__ void load_keys(const Pages &pages, uint64_t codes, uint64_t scales, int c, int g,
+template <int NB, class P>
+__device__ __forceinline__ void load_keys(const P &pages, uint64_t codes, uint64_t scales, int c, int g,
                                           unsigned (&k)[NB], unsigned (&ks)[NB == 8 ? 2 : 1])
 {
     const int size = pages.size;
@@ -496,8 +499,23 @@ __device__ __forceinline__ void load_keys(const Pages &pages, uint64_t codes, ui
         ks[1] = sc[size];
 }
 
+// Codes of channels [2 NB c, 2 NB (c + 1)) of one position.
 template <int NB>
-__device__ __forceinline__ void load_tile(Pages &pages, int i, int c, int g, RawTile<NB> &r)
+__device__ __forceinline__ void load_value(const uint8_t *src, unsigned (&v)[NB == 8 ? 2 : 1])
+{
+    if constexpr (NB == 2) {
+        v[0] = *(const uint16_t *)src;
+    } else if constexpr (NB == 4) {
+        v[0] = *(const unsigned *)src;
+    } else {
+        const u32x2 w = *(const u32x2 *)src;
+        v[0] = w[0];
+        v[1] = w[1];
+    }
+}
+
+template <int NB>
+__device__ __forceinline__ void load_tile(Pages<2> &pages, int i, int c, int g, RawTile<NB> &r)
 {
     int page[2];
     pages.take(page);
@@ -506,19 +524,9 @@ __device__ __forceinline__ void load_tile(Pages &pages, int i, int c, int g, Raw
         uint64_t codes, scales;
         r.there[h] = pages.at(i, h, page[h], 16 * NB, codes, scales);
         load_keys<NB>(pages, codes, scales, c, g, r.k[h], r.ks[h]);
-        const uint8_t *v = pages.vq + codes + (unsigned)(4 * g * (NB * 16) + c * NB);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if constexpr (NB == 2) {
-                r.v[4 * h + k][0] = *(const uint16_t *)(v + k * (NB * 16));
-            } else if constexpr (NB == 4) {
-                r.v[4 * h + k][0] = *(const unsigned *)(v + k * (NB * 16));
-            } else {
-                const u32x2 w = *(const u32x2 *)(v + k * (NB * 16));
-                r.v[4 * h + k][0] = w[0];
-                r.v[4 * h + k][RawTile<NB>::kVW - 1] = w[1];
-            }
-        }
+        for (int k = 0; k < 4; ++k)
+            load_value<NB>(pages.vq + codes + (unsigned)((4 * g + k) * (NB * 16) + c * NB), r.v[4 * h + k]);
         r.vs[h] = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
     }
 }
@@ -536,18 +544,9 @@ __device__ __forceinline__ unsigned cvt_byte(unsigned raw, float sc, int b)
     return __builtin_bit_cast(unsigned, v);
 }
 
-// (channel 2b, channel 2b + 1) of eight positions -> each channel's eight positions.
-__device__ __forceinline__ void regroup(const unsigned (&w)[8], bf16x8 &even, bf16x8 &odd)
-{
-    u32x4 e, o;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        e[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x05040100u);
-        o[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x07060302u);
-    }
-    even = __builtin_bit_cast(bf16x8, e);
-    odd = __builtin_bit_cast(bf16x8, o);
-}
+// (channel 2b, channel 2b + 1) of two positions -> each channel's two positions.
+__device__ __forceinline__ unsigned even_of(unsigned w0, unsigned w1) { return __builtin_amdgcn_perm(w1, w0, 0x05040100u); }
+__device__ __forceinline__ unsigned odd_of(unsigned w0, unsigned w1) { return __builtin_amdgcn_perm(w1, w0, 0x07060302u); }
 
 // Few columns (NB = dim / 32; kNQ tiles of 16): every wave has the same
 // columns and takes every kWaves-th cache tile, straight from memory.
@@ -563,7 +562,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R, c, g, q);
     int i = w.begin + wave;
-    Pages pages(a, w, lane, i, kWaves);
+    Pages<2> pages(a, w, lane, i, kWaves, 0);
 
     // codes one tile ahead
     RawTile<NB> next;
@@ -623,13 +622,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[k] = cvt_byte(r.v[k][NB == 8 ? b / 4 : 0], scale_operand(vsb[k]), b & 3);
-            bf16x8 even, odd;
-            regroup(v, even, odd);
+            u32x4 even, odd;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                even[k] = even_of(v[2 * k], v[2 * k + 1]);
+                odd[k] = odd_of(v[2 * k], v[2 * k + 1]);
+            }
 #pragma unroll
             for (int n = 0; n < kNQ; ++n) {
-                q.acc[n][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, P[n], q.acc[n][2 * b], 0, 0, 0);
-                q.acc[n][2 * b + 1] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, P[n], q.acc[n][2 * b + 1], 0, 0, 0);
+                q.acc[n][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), P[n],
+                                                                          q.acc[n][2 * b], 0, 0, 0);
+                q.acc[n][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), P[n],
+                                                                              q.acc[n][2 * b + 1], 0, 0, 0);
             }
         }
         // the channels of a lane share a block, so one count serves them all
@@ -695,15 +699,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
 // Many columns: the waves have columns of their own and share the cache tiles
 // through LDS, 64 positions at a time in two stages, already converted: each
 // wave converts a quarter, in the order in which the products read it (one
-// 16-byte piece per lane and operand, so neither side has a bank conflict).
-// Per wave and 32 positions that leaves a quarter of the conversions (24 of
-// 96 vector instructions at dim 128) next to its own softmax.
+// 16-byte piece per lane and operand).  Per wave and 32 positions that
+// leaves a quarter of the conversions (24 of 96 vector instructions at dim
+// 128) next to its own softmax.
 template <int NB>
 struct __align__(16) WideStage {
-    u32x4 k[4][NB][64];     // 16 positions each
-    u32x4 v[2][2 * NB][64]; // 32 positions each
-    unsigned char nan[2][64]; // per lane: the slots whose V block was NaN (stored as zeros)
-    unsigned flags[2];        // 1 some of nan is set; 2 and 4 the tile's halves have a page
+    u32x4 k[kWaves][NB][64];        // 16 positions each
+    u32x2 v[2][2 * NB][64][2];      // 32 positions each, a half in 8 bytes
+    unsigned flags[kWaves];         // of the wave that wrote: 1 some of nan is set, 2 its half has a page
+    unsigned char nan[kWaves][64];  // per lane: the slots whose V block was NaN (stored as zeros)
 };
 
 template <int NB, int kNQ>
@@ -721,75 +725,61 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     load_columns<NB, kNQ>(a, w, w.local * R + wave * kNQ * 16, c, g, q);
     const int end = w.t.pmax < 0 ? 0 : w.t.pmax + 1 < w.t.span ? w.t.pmax + 1 : w.t.span; // of all columns
 
-    // This wave's quarter of a stage: tile `wave / 2` of the two, its keys'
-    // half wave % 2, and of its values the channel bytes' half wave % 2.
+    // This wave's quarter of a stage: half `part` of tile `mine` of the two.
     const int mine = wave >> 1, part = wave & 1;
-    unsigned k[NB], ks[NB == 8 ? 2 : 1], v[8], vs[2];
-    bool there[2];
-    Pages pages(a, w, lane, w.begin + mine, 2);
+    unsigned k[NB], ks[NB == 8 ? 2 : 1], v[4][NB == 8 ? 2 : 1], vs;
+    bool there;
+    Pages<1> pages(a, w, lane, w.begin + mine, 2, part);
     auto clamp = [&](int i) { return i < w.stop ? i : w.stop - 1; };
     auto load = [&](int i) {
-        int page[2];
+        int page[1];
         pages.take(page);
+        uint64_t codes, scales;
+        there = pages.at(i, part, page[0], 16 * NB, codes, scales);
+        load_keys<NB>(pages, codes, scales, c, g, k, ks);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint64_t codes, scales;
-            there[h] = pages.at(i, h, page[h], 16 * NB, codes, scales);
-            if (h == part)
-                load_keys<NB>(pages, codes, scales, c, g, k, ks);
-            const uint8_t *src = pages.vq + codes + (unsigned)(4 * g * (NB * 16) + c * NB) + (NB == 8 ? 4 * part : 0);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                v[4 * h + x] = NB == 2 ? (unsigned)*(const uint16_t *)(src + x * (NB * 16))
-                                       : *(const unsigned *)(src + x * (NB * 16));
-            vs[h] = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
-        }
+        for (int x = 0; x < 4; ++x)
+            load_value<NB>(pages.vq + codes + (unsigned)((4 * g + x) * (NB * 16) + c * NB), v[x]);
+        vs = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
     };
     auto convert = [&](int i, WideStage<NB> &st) {
 #pragma unroll
         for (int p = 0; p < NB; ++p)
             st.k[wave][p][lane] =
                 __builtin_bit_cast(u32x4, mx_bf16x8(k[p], scale_operand(ks[NB == 8 ? p / 4 : 0])));
-        const int j0 = pages.tile(i) * kTile;
-        unsigned vsb[8], slots = 0;
+        const int j0 = pages.tile(i) * kTile + 16 * part;
+        unsigned vsb[4], slots = 0;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            vsb[x] = (vs[x >> 2] >> (8 * (x & 3))) & 0xFFu;
-            if (NB != 8)
-                v[x] >>= part ? 4 * NB : 0;
-        }
+        for (int x = 0; x < 4; ++x)
+            vsb[x] = (vs >> (8 * x)) & 0xFFu;
         // a scale byte 0xFF: its low seven bits carry into the eighth, which is set
-        const unsigned ff = ((((vs[0] & 0x7F7F7F7Fu) + 0x01010101u) & vs[0]) | (((vs[1] & 0x7F7F7F7Fu) + 0x01010101u) & vs[1])) & 0x80808080u;
-        const bool odd_tile = j0 + kTile > end || !there[0] || !there[1];
-        if (odd_tile || __builtin_amdgcn_ballot_w64(ff != 0)) {
+        const bool nans = __builtin_amdgcn_ballot_w64(((vs & 0x7F7F7F7Fu) + 0x01010101u) & vs & 0x80808080u) != 0;
+        if (j0 + 16 > end || !there || nans) {
             // cleared: positions that no column sees, as in
             // attention_few_kernel, and NaN blocks, which are noted
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int h = x >> 2;
-                const bool dead = j0 + 16 * h + 4 * g + (x & 3) >= end || !there[h], nan = vsb[x] == 0xFFu;
+            for (int x = 0; x < 4; ++x) {
+                const bool dead = j0 + 4 * g + x >= end || !there, nan = vsb[x] == 0xFFu;
                 slots |= (unsigned)(nan && !dead) << x;
                 vsb[x] = dead || nan ? 127 : vsb[x];
-                v[x] = dead || nan ? 0 : v[x];
+#pragma unroll
+                for (int y = 0; y < (NB == 8 ? 2 : 1); ++y)
+                    v[x][y] = dead || nan ? 0 : v[x][y];
             }
         }
 #pragma unroll
-        for (int b = 0; b < NB / 2; ++b) {
-            unsigned x[8];
+        for (int b = 0; b < NB; ++b) {
+            unsigned x[4];
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
-                x[y] = cvt_byte(v[y], scale_operand(vsb[y]), b);
-            bf16x8 even, odd;
-            regroup(x, even, odd);
-            st.v[mine][part * NB + 2 * b][lane] = __builtin_bit_cast(u32x4, even);
-            st.v[mine][part * NB + 2 * b + 1][lane] = __builtin_bit_cast(u32x4, odd);
+            for (int y = 0; y < 4; ++y)
+                x[y] = cvt_byte(v[y][NB == 8 ? b / 4 : 0], scale_operand(vsb[y]), b & 3);
+            st.v[mine][2 * b][lane][part] = (u32x2){even_of(x[0], x[1]), even_of(x[2], x[3])};
+            st.v[mine][2 * b + 1][lane][part] = (u32x2){odd_of(x[0], x[1]), odd_of(x[2], x[3])};
         }
-        if (part == 0) { // both of the tile's waves know this
-            const bool any = __builtin_amdgcn_ballot_w64(slots != 0) != 0;
-            st.nan[mine][lane] = (unsigned char)slots;
-            if (lane == 0)
-                st.flags[mine] = (unsigned)any | (unsigned)there[0] << 1 | (unsigned)there[1] << 2;
-        }
+        const bool any = __builtin_amdgcn_ballot_w64(slots != 0) != 0;
+        st.nan[wave][lane] = (unsigned char)slots;
+        if (lane == 0)
+            st.flags[wave] = (unsigned)any | (unsigned)there << 1;
     };
 
     int i = w.begin;
@@ -811,8 +801,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
             const int j0 = pages.tile(i + u) * kTile;
             if (i + u >= w.stop || j0 >= q.whi)
                 continue;
-            const unsigned flags = (unsigned)__builtin_amdgcn_readfirstlane((int)st.flags[u]);
-            const bool has[2] = {(flags & 2u) != 0, (flags & 4u) != 0};
+            const unsigned f0 = (unsigned)__builtin_amdgcn_readfirstlane((int)st.flags[2 * u]);
+            const unsigned f1 = (unsigned)__builtin_amdgcn_readfirstlane((int)st.flags[2 * u + 1]);
+            const bool has[2] = {(f0 & 2u) != 0, (f1 & 2u) != 0};
             const bool full = has[0] && has[1] && sees_all<NB, kNQ>(a, q, j0, w.t.span);
             f32x4 S[kNQ][2];
 #pragma unroll
@@ -828,20 +819,31 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
                         S[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q.Q[n][p], S[n][h], 0, 0, 0);
                 }
             }
+            // LDS reads four operands ahead of the products
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int x = 0; x < 2 * NB; ++x) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kNQ, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
             unsigned seen[kNQ];
             if (!full)
                 mask_scores<NB, kNQ>(a, q, j0, w.t.span, has, g, S, seen);
-            bf16x8 P[kNQ];
+            // the first operands of the second product, read under the softmax
+            bf16x8 P[kNQ], early[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                early[j] = __builtin_bit_cast(bf16x8, *(const u32x4 *)st.v[u][j][lane]);
             weigh<NB, kNQ>(a, q, S, P);
 #pragma unroll
             for (int j = 0; j < 2 * NB; ++j) {
-                const bf16x8 vf = __builtin_bit_cast(bf16x8, st.v[u][j][lane]);
+                const bf16x8 vf = j < 4 ? early[j] : __builtin_bit_cast(bf16x8, *(const u32x4 *)st.v[u][j][lane]);
 #pragma unroll
                 for (int n = 0; n < kNQ; ++n)
                     q.acc[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, P[n], q.acc[n][j], 0, 0, 0);
             }
-            if (flags & 1u) {
-                const unsigned slots = st.nan[u][lane];
+            if ((f0 | f1) & 1u) {
+                const unsigned slots = st.nan[2 * u][lane] | (unsigned)st.nan[2 * u + 1][lane] << 4;
 #pragma unroll
                 for (int n = 0; n < kNQ; ++n) {
                     const f32x4 count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
