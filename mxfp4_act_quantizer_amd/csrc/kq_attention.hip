@@ -173,17 +173,16 @@ struct Place {
     int begin, stop; // its share of the plan's cache tiles
 };
 
-// workgroup -> (split, column tile, head), the head fastest: the eight XCDs
+// Workgroup id -> (split, column tile, head), the head fastest: the eight XCDs
 // take workgroups in turn, so a head's cache stays in few L2s.  The last
 // column tiles, whose rows see most, start first.  False: nothing to do.
-__device__ __forceinline__ bool find_work(const AttnArgs &a, int R, int lane, Place &w)
+__device__ __forceinline__ bool find_work(const AttnArgs &a, int R, int id, int splits, int lane, Place &w)
 {
     const int heads = (int)a.c.heads;
-    int id = (int)blockIdx.x;
     w.head = id % heads;
     id /= heads;
-    w.split = id % a.splits;
-    const int tile = a.tiles - 1 - id / a.splits;
+    w.split = id % splits;
+    const int tile = a.tiles - 1 - id / splits;
     // the tiles of sequence s start at row_start[s] group / R + s, which leaves
     // it at least ceil(columns / R)
     auto first_of = [&](int s) {
@@ -557,7 +556,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
     const int c = lane & 15, g = lane >> 4;
     constexpr int R = 16 * kNQ;
     Place w;
-    if (!find_work(a, R, lane, w))
+    if (!find_work(a, R, (int)blockIdx.x, a.splits, lane, w))
         return;
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R, c, g, q);
@@ -719,7 +718,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     extern __shared__ __align__(16) unsigned char lds[];
     WideStage<NB> *stage = (WideStage<NB> *)lds;
     Place w;
-    if (!find_work(a, R, lane, w))
+    if (!find_work(a, R, (int)blockIdx.x, a.splits, lane, w))
         return;
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R + wave * kNQ * 16, c, g, q);
@@ -829,12 +828,16 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
             unsigned seen[kNQ];
             if (!full)
                 mask_scores<NB, kNQ>(a, q, j0, w.t.span, has, g, S, seen);
-            // the first operands of the second product, read under the softmax
+            // the softmax gives way to the products of the other waves of its
+            // SIMD (2048-token chunk: 590 -> 569 us); the first operands of
+            // the second product are read under it
+            __builtin_amdgcn_s_setprio(0);
             bf16x8 P[kNQ], early[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 early[j] = __builtin_bit_cast(bf16x8, *(const u32x4 *)st.v[u][j][lane]);
             weigh<NB, kNQ>(a, q, S, P);
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int j = 0; j < 2 * NB; ++j) {
                 const bf16x8 vf = j < 4 ? early[j] : __builtin_bit_cast(bf16x8, *(const u32x4 *)st.v[u][j][lane]);
@@ -842,6 +845,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
                 for (int n = 0; n < kNQ; ++n)
                     q.acc[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, P[n], q.acc[n][j], 0, 0, 0);
             }
+            if constexpr (NB > 2)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB - 4, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 2 * NB * kNQ, 0);
             if ((f0 | f1) & 1u) {
                 const unsigned slots = st.nan[2 * u][lane] | (unsigned)st.nan[2 * u + 1][lane] << 4;
 #pragma unroll
@@ -861,55 +867,53 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     store_columns<NB, kNQ>(a, w, q, g);
 }
 
-// Joins the splits of one row and head: a workgroup of 256 threads, dim / 4
-// of them along the channels and the rest along the splits.
+// Joins the splits of the column tiles that have several: `per_tile`
+// workgroups of 256 threads for each column tile and head, `cols` columns at a
+// time; of the threads of a column dim / 4 lie along its channels and the rest
+// along the splits.
 template <int NB>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R)
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, int per_tile, int cols)
 {
-    constexpr int dim = 32 * NB, along = dim / 4, ways = 256 / along;
-    const int lane = threadIdx.x & 63;
-    const int head = (int)(blockIdx.x % (unsigned)a.q_heads);
-    const int row = (int)(blockIdx.x / (unsigned)a.q_heads);
-    const int s = wave_search((int)a.b.seqs, row, lane, [&](int i) { return (int64_t)a.b.row_start[i]; });
-    const SeqRows q = seq_rows(a.b, s);
-    if (row < q.first || row >= q.first + q.rows)
-        return;
-    const int col = (row - q.first) * a.group + head % a.group;
-    TilePlan t;
-    plan_tile(a, s, col / R, R, lane, t);
-    if (t.splits == 1)
-        return;
-    const int64_t at0 = (int64_t)row * a.q_heads + head, step = a.b.rows * a.q_heads;
-    float m = -__builtin_inff();
-    for (int i = lane; i < t.splits; i += 64)
-        m = __builtin_fmaxf(m, a.part_ml[(at0 + i * step) * 2]);
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1)
-        m = __builtin_fmaxf(m, __shfl_xor(m, x, 64));
-    const int d4 = threadIdx.x % along, way = threadIdx.x / along;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
-    for (int i = way; i < t.splits; i += ways) {
-        const f32x2 ml = *(const f32x2 *)(a.part_ml + (at0 + i * step) * 2);
-        const float f = ml[0] == m ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - m);
-        o += f * *(const f32x4 *)(a.part_o + (at0 + i * step) * dim + d4 * 4);
-        l += f * ml[1];
-    }
+    constexpr int dim = 32 * NB, along = dim / 4;
     __shared__ f32x4 so[256];
     __shared__ float sl[256];
-    so[threadIdx.x] = o;
-    sl[threadIdx.x] = l;
-    __syncthreads();
-    if (way)
+    const int lane = threadIdx.x & 63;
+    const int part = (int)(blockIdx.x % (unsigned)per_tile);
+    Place w;
+    if (!find_work(a, R, (int)(blockIdx.x / (unsigned)per_tile), 1, lane, w) || w.t.splits == 1)
         return;
-#pragma unroll
-    for (int w = 1; w < ways; ++w) {
-        o += so[w * along + d4];
-        l += sl[w * along + d4];
+    const int ways = 256 / along / cols; // threads along the splits
+    const int d4 = threadIdx.x % along, way = threadIdx.x / along % ways, sub = threadIdx.x / along / ways;
+    const int stop = (w.local + 1) * R < w.t.cols ? (w.local + 1) * R : w.t.cols;
+    const int64_t step = a.b.rows * a.q_heads;
+    for (int col0 = w.local * R + part * cols; col0 < stop; col0 += per_tile * cols) {
+        const int col = col0 + sub < stop ? col0 + sub : stop - 1;
+        const int i = col / a.group, row = w.t.seq.first + i, head = w.head * a.group + col - i * a.group;
+        const int64_t at = (int64_t)row * a.q_heads + head;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        float l = 0.0f, m = -__builtin_inff();
+        for (int x = 0; x < w.t.splits; ++x)
+            m = vmax(m, a.part_ml[(at + x * step) * 2]);
+        for (int x = way; x < w.t.splits; x += ways) {
+            const f32x2 ml = *(const f32x2 *)(a.part_ml + (at + x * step) * 2);
+            const float f = ml[0] == m ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - m);
+            o += f * *(const f32x4 *)(a.part_o + (at + x * step) * dim + d4 * 4);
+            l += f * ml[1];
+        }
+        so[threadIdx.x] = o;
+        sl[threadIdx.x] = l;
+        __syncthreads();
+        if (way == 0 && col0 + sub < stop) {
+            for (int x = 1; x < ways; ++x) {
+                o += so[threadIdx.x + x * along];
+                l += sl[threadIdx.x + x * along];
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            *(u32x2 *)(a.out + (int64_t)row * a.out_stride + head * dim + d4 * 4) =
+                (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        }
+        __syncthreads();
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    *(u32x2 *)(a.out + (int64_t)row * a.out_stride + head * dim + d4 * 4) =
-        (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 // Columns of a workgroup, and how its waves share them.
@@ -928,7 +932,8 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
     s.nq = mean <= 16 || c.dim == 256 ? 1 : 2;
     s.R = 16 * s.nq * (s.many ? kWaves : 1);
     s.tiles = (int)(cols / s.R + b.seqs);
-    s.wanted = (s.many ? 2 : 4) * device_cus();
+    // workgroups that are resident together: few columns by registers, many by LDS
+    s.wanted = (s.many ? (c.dim == 64 ? 4 : c.dim == 128 ? 2 : 1) : 4) * device_cus();
     s.splits = 1;
     const int64_t groups = (int64_t)s.tiles * c.heads;
     if (b.seqs <= kSplitSeqs && 2 * groups <= s.wanted) {
@@ -968,7 +973,15 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1)
         return e;
-    attention_join_kernel<NB><<<dim3((unsigned)(a.b.rows * a.q_heads)), dim3(256), 0, stream>>>(a, s.R);
+    // about 2048 workgroups (8 a CU), each with the columns abreast that leave
+    // a thread for every split
+    int cols = 256 / (8 * NB);
+    while (cols > 1 && 256 / (8 * NB) / cols < s.splits)
+        cols /= 2;
+    const int64_t groups = (int64_t)s.tiles * a.c.heads, chunks = (s.R + cols - 1) / cols;
+    int64_t per = 2048 / groups;
+    per = per < 1 ? 1 : per > chunks ? chunks : per;
+    attention_join_kernel<NB><<<dim3((unsigned)(groups * per)), dim3(256), 0, stream>>>(a, s.R, (int)per, cols);
     return hipGetLastError();
 }
 
