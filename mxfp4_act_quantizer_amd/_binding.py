@@ -9,6 +9,7 @@ built, importing this module raises.
 import collections
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -76,15 +77,9 @@ def _tuning(tuning):
     return ctypes.byref(Tuning(**{k: int(v) for k, v in tuning.items()}))
 
 
-class _CacheArg(ctypes.Structure):  # mx_cache in kroquant.h
-    _fields_ = [("kq", _P), ("ks", _P), ("vq", _P), ("vs", _P), ("pages", _I64), ("page_size", _I64),
-                ("heads", _I64), ("dim", _I64)]
-
-
-class _BatchArg(ctypes.Structure):  # mx_batch in kroquant.h
-    _fields_ = [("page_table", _P), ("row_start", _P), ("lengths", _P), ("seqs", _I64), ("width", _I64),
-                ("rows", _I64)]
-
+# mx_cache and mx_batch of kroquant.h as the bytes that a call is given
+_CACHE = struct.Struct("8q")  # kq, ks, vq, vs, pages, page_size, heads, dim
+_BATCH = struct.Struct("6q")  # page_table, row_start, lengths, seqs, width, rows
 
 _lib.kq_quantize.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _P]
 _lib.kq_quantize_ex.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _INT, _P]
@@ -500,8 +495,9 @@ def mx_cache_new(pages, page_size, heads, dim, device="cuda"):
 
 
 # These calls are short enough on the GPU that the host side counts: the checks
-# below take the tensor's own attributes one at a time, and the raw handle of
-# the current stream rather than a new Stream object.
+# below take the tensors' own attributes one at a time, structs are packed as
+# bytes, and the stream is the current one's raw handle rather than a new
+# Stream object.
 def _gpu(t, dtype, name):
     """Address of a contiguous GPU tensor of the dtype."""
     if t.dtype is dtype and t.is_cuda and t.is_contiguous():
@@ -518,16 +514,17 @@ def _call(fn, where, stream, tensors, *args):
     """fn(*args, stream) with the tensors' device current (they share one)."""
     torch = _torch()
     dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"{where}: tensors lie on cuda:{dev} and {t.device}")
+    if torch._C._cuda_getDeviceCount() > 1:
+        for t in tensors:
+            if t.get_device() != dev:
+                raise ValueError(f"{where}: tensors lie on cuda:{dev} and {t.device}")
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device.index != dev:
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
     else:
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -543,7 +540,7 @@ def _heads_view(t, name, heads, dim):
         raise TypeError(f"{name} must be a torch tensor on the GPU")
     if t.dtype not in _bf16_types():
         raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+    if t.dim() != 3 or t.shape[1:] != (heads, dim):
         raise ValueError(f"{name} must be [rows, {heads}, {dim}], is {list(t.shape)}")
     row, head, one = t.stride()
     if one != 1 or (heads > 1 and head != dim):
@@ -552,6 +549,7 @@ def _heads_view(t, name, heads, dim):
 
 
 def _cache_arg(cache):
+    """(mx_cache, heads, dim)"""
     u8 = _torch().uint8
     kq, ks, vq, vs = cache
     if kq.dim() != 4:
@@ -560,17 +558,18 @@ def _cache_arg(cache):
     if vq.shape != kq.shape or ks.shape != vs.shape or ks.shape != (pages, heads, half // 16, size):
         raise ValueError("the cache's buffers do not match: codes [pages, heads, page_size, dim/2], scales "
                          "[pages, heads, dim/32, page_size]")
-    return _CacheArg(_gpu(kq, u8, "cache.kq"), _gpu(ks, u8, "cache.ks"), _gpu(vq, u8, "cache.vq"),
-                     _gpu(vs, u8, "cache.vs"), pages, size, heads, half * 2)
+    return _CACHE.pack(_gpu(kq, u8, "cache.kq"), _gpu(ks, u8, "cache.ks"), _gpu(vq, u8, "cache.vq"),
+                       _gpu(vs, u8, "cache.vs"), pages, size, heads, half * 2), heads, half * 2
 
 
 def _batch_arg(page_table, row_start, lengths, rows):
+    """mx_batch"""
     i32 = _torch().int32
     seqs = lengths.numel()
     if page_table.dim() != 2 or page_table.shape[0] != seqs or row_start.numel() != seqs + 1:
         raise ValueError("a batch is page_table [seqs, width], row_start [seqs + 1], lengths [seqs]")
-    return _BatchArg(_gpu(page_table, i32, "page_table"), _gpu(row_start, i32, "row_start"),
-                     _gpu(lengths, i32, "lengths"), seqs, page_table.shape[1], rows)
+    return _BATCH.pack(_gpu(page_table, i32, "page_table"), _gpu(row_start, i32, "row_start"),
+                       _gpu(lengths, i32, "lengths"), seqs, page_table.shape[1], rows)
 
 
 def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
@@ -599,9 +598,9 @@ def mx_cache_write(k, v, cache, page_table, row_start, lengths, factors=None, st
     free) of a step into their slots of the cache; `factors` [nT, 5, 2, 2]
     puts the keys through the Kronecker transform first.  Row r of sequence i
     is position lengths[i] - row_start[i + 1] + r."""
-    c = _cache_arg(cache)
-    kp, kst = _heads_view(k, "k", c.heads, c.dim)
-    vp, vst = _heads_view(v, "v", c.heads, c.dim)
+    c, heads, dim = _cache_arg(cache)
+    kp, kst = _heads_view(k, "k", heads, dim)
+    vp, vst = _heads_view(v, "v", heads, dim)
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     b = _batch_arg(page_table, row_start, lengths, k.shape[0])
@@ -610,8 +609,7 @@ def mx_cache_write(k, v, cache, page_table, row_start, lengths, factors=None, st
     if factors is not None:
         fp, nT = _gpu(factors, _torch().float32, "factors"), _nT(factors)
         tensors += (factors,)
-    _call(_lib.mx_cache_write, "mx_cache_write", stream, tensors, kp, kst, vp, vst, fp, nT, ctypes.byref(c),
-          ctypes.byref(b))
+    _call(_lib.mx_cache_write, "mx_cache_write", stream, tensors, kp, kst, vp, vst, fp, nT, c, b)
 
 
 def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=None, stream=None):
@@ -619,28 +617,27 @@ def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=No
     cache's codes stand for them.  `rows` sizes the outputs allocated here;
     rows of no sequence, or without a slot, are left as they were."""
     torch = _torch()
-    c = _cache_arg(cache)
+    c, heads, dim = _cache_arg(cache)
     if rows is None:
         if k is None:
             raise ValueError("give rows, or k and v")
         rows = k.shape[0]
-    shape = (int(rows), c.heads, c.dim)
+    shape = (int(rows), heads, dim)
     if k is None:
         k = torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device)
+        v = torch.empty_like(k)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {list(shape)}")
     b = _batch_arg(page_table, row_start, lengths, shape[0])
     _call(_lib.mx_cache_read, "mx_cache_read", stream, (k, v, *cache, page_table, row_start, lengths),
-          ctypes.byref(c), ctypes.byref(b), _gpu_bf16(k, "k"), _gpu_bf16(v, "v"))
+          c, b, _gpu_bf16(k, "k"), _gpu_bf16(v, "v"))
     return k, v
 
 
 def _attention_bytes(q_heads, c, b, window, sinks):
     need = _I64()
-    st = _lib.mx_cache_attention_workspace(q_heads, ctypes.byref(c), ctypes.byref(b), window, sinks,
-                                           ctypes.byref(need))
+    st = _lib.mx_cache_attention_workspace(q_heads, c, b, window, sinks, ctypes.byref(need))
     if st:
         raise KQError(st, "mx_cache_attention")
     return need.value
@@ -650,7 +647,7 @@ def mx_cache_attention_workspace(rows, q_heads, cache, page_table, row_start, le
     """Bytes of workspace that mx_cache_attention asks for (it depends on the
     sizes only, not on the lengths)."""
     with _torch().cuda.device(cache.kq.device):
-        return _attention_bytes(int(q_heads), _cache_arg(cache),
+        return _attention_bytes(int(q_heads), _cache_arg(cache)[0],
                                 _batch_arg(page_table, row_start, lengths, int(rows)), int(window), int(sinks))
 
 
@@ -664,21 +661,23 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
     `workspace` is a uint8 tensor of mx_cache_attention_workspace bytes
     (allocated here when not given)."""
     torch = _torch()
-    c = _cache_arg(cache)
+    c, _, dim = _cache_arg(cache)
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, dim]")
     rows, heads, _ = q.shape
-    qp, qst = _heads_view(q, "q", heads, c.dim)
+    qp, qst = _heads_view(q, "q", heads, dim)
     if out is None:
-        out = torch.empty((rows, heads, c.dim), dtype=torch.bfloat16, device=q.device)
-    elif out.shape[0] != rows:
-        raise ValueError("out must have q's rows")
-    op, ost = _heads_view(out, "out", heads, c.dim)
+        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=q.device)
+        op, ost = out.data_ptr(), heads * dim
+    else:
+        if out.shape[0] != rows:
+            raise ValueError("out must have q's rows")
+        op, ost = _heads_view(out, "out", heads, dim)
     b = _batch_arg(page_table, row_start, lengths, rows)
     tensors = (q, out, *cache, page_table, row_start, lengths)
     if workspace is None:
         # the size goes by the compute units of the current device: the tensors' one
-        if torch.cuda.current_device() == q.get_device():
+        if torch._C._cuda_getDevice() == q.get_device():
             need = _attention_bytes(heads, c, b, window, sinks)
         else:
             with torch.cuda.device(q.device):
@@ -691,8 +690,8 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
         tensors += (workspace,)
     if workspace is not None:
         wp = _gpu(workspace, torch.uint8, "workspace")
-    _call(_lib.mx_cache_attention, "mx_cache_attention", stream, tensors, qp, qst, heads, ctypes.byref(c),
-          ctypes.byref(b), c.dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, ost, wp, need)
+    _call(_lib.mx_cache_attention, "mx_cache_attention", stream, tensors, qp, qst, heads, c, b,
+          dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, ost, wp, need)
     return out
 
 

@@ -5,7 +5,17 @@ import ctypes
 import pytest
 
 import mxfp4_act_quantizer_amd as K
-from mxfp4_act_quantizer_amd import _binding as B
+
+
+class CacheArg(ctypes.Structure):  # mx_cache in kroquant.h
+    _fields_ = [(f, ctypes.c_void_p) for f in ("kq", "ks", "vq", "vs")] + [
+        (f, ctypes.c_int64) for f in ("pages", "page_size", "heads", "dim")]
+
+
+class BatchArg(ctypes.Structure):  # mx_batch
+    _fields_ = [(f, ctypes.c_void_p) for f in ("page_table", "row_start", "lengths")] + [
+        (f, ctypes.c_int64) for f in ("seqs", "width", "rows")]
+
 
 FAKE = 1 << 40  # never dereferenced: every call below fails validation first
 GIB = 1 << 30
@@ -18,13 +28,13 @@ def raw(name, *args):
 def cache(**kw):
     c = dict(kq=FAKE, ks=FAKE + GIB, vq=FAKE + 2 * GIB, vs=FAKE + 3 * GIB, pages=10, page_size=16, heads=2, dim=64)
     c.update(kw)
-    return ctypes.byref(B._CacheArg(**c))
+    return ctypes.byref(CacheArg(**c))
 
 
 def batch(**kw):
     b = dict(page_table=FAKE + 4 * GIB, row_start=FAKE + 5 * GIB, lengths=FAKE + 6 * GIB, seqs=3, width=4, rows=7)
     b.update(kw)
-    return ctypes.byref(B._BatchArg(**b))
+    return ctypes.byref(BatchArg(**b))
 
 
 def test_gemv_refusals():
@@ -93,6 +103,39 @@ def test_cache_write_strides_and_factors():
     # the last row of a strided view counts: 6 rows apart and one more
     end = FAKE + 7 * GIB + 2 * (6 * 1024 + 128)
     assert call(ks=1024, c=cache(ks=end - 16)) == K.KQ_ERR_OVERLAP
+
+
+def test_attention_refusals():
+    q, out, work = FAKE + 7 * GIB, FAKE + 8 * GIB, FAKE + 9 * GIB
+
+    def call(c=None, b=None, q=q, qs=512, heads=8, scale=0.125, window=0, sinks=0, out=out, os=512, work=work,
+             size=1 << 20):
+        return raw("mx_cache_attention", q, qs, heads, c or cache(), b or batch(), ctypes.c_float(scale), window, sinks,
+                   out, os, work, size, None)
+
+    for dim in (32, 96, 160, 192):
+        assert call(cache(dim=dim), qs=2048, os=2048) == K.KQ_ERR_SHAPE, dim
+    assert call(cache(pages=0)) == call(b=batch(rows=-1)) == call(b=batch(lengths=None)) == K.KQ_ERR_ARG
+    assert call(heads=0) == call(window=-1) == call(sinks=-1) == call(size=-1) == K.KQ_ERR_ARG
+    assert call(heads=7) == call(heads=4098) == call(window=(1 << 30) + 1) == call(sinks=(1 << 30) + 1) == K.KQ_ERR_SHAPE
+    assert call(heads=4096, b=batch(rows=1 << 19), qs=1 << 18, os=1 << 18) == K.KQ_ERR_SHAPE
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e-31):
+        assert call(scale=scale) == K.KQ_ERR_ARG, scale
+    assert call(q=None) == call(out=None) == K.KQ_ERR_ARG
+    assert call(q=q + 8) == call(out=out + 4) == call(work=work + 8) == K.KQ_ERR_ALIGN
+    assert call(qs=511) == call(os=448) == K.KQ_ERR_SHAPE
+    assert call(qs=516) == call(os=513) == K.KQ_ERR_ALIGN
+    assert call(out=q + 64) == call(out=FAKE + 16) == call(work=FAKE + 3 * GIB) == call(work=out) == K.KQ_ERR_OVERLAP
+    assert call(b=batch(row_start=out + 64)) == call(b=batch(page_table=work)) == K.KQ_ERR_OVERLAP
+    assert call(b=batch(rows=0), q=None, out=None, work=None) == call(b=batch(seqs=0), q=None) == K.KQ_OK
+    need = ctypes.c_int64(-1)
+
+    def bytes_of(heads=8, c=None, b=None, window=0, to=ctypes.byref(need)):
+        return raw("mx_cache_attention_workspace", heads, c or cache(), b or batch(), window, 0, to)
+
+    assert bytes_of(to=None) == bytes_of(window=-1) == K.KQ_ERR_ARG
+    assert bytes_of(heads=3) == bytes_of(c=cache(dim=96)) == K.KQ_ERR_SHAPE
+    assert bytes_of(b=batch(rows=0)) == K.KQ_OK and need.value == 0
 
 
 def test_binding_checks():
