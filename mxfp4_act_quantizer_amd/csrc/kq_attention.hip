@@ -52,75 +52,46 @@ constexpr int kTile = 32;  // cache positions of a step
 constexpr int kWaves = 4;  // of a workgroup
 constexpr float kRaise = 8.0f; // log2 of how far a score may exceed the scaling maximum
 constexpr int kMaxSplits = 128;
-constexpr int kSplitSeqs = 256; // with more sequences there is work enough without splitting
 
 struct AttnArgs {
     const uint16_t *q;
     uint16_t *out;
-    float *part_o; // [splits][rows][q_heads][dim] unnormalised outputs
-    float *part_ml; // [splits][rows][q_heads][2] maximum (log2) and sum
+    float *part_o;  // [parts][dim] unnormalised outputs of columns
+    float *part_ml; // [parts][2] their maxima (log2) and sums
     int64_t q_stride, out_stride;
     mx_cache c;
     mx_batch b;
     int q_heads, group;
     int window, sinks;
     float scale2; // scale * log2(e)
-    int splits;   // most splits of a sequence
+    int splits;   // many columns: most splits of a sequence
     int wanted;   // workgroups that fill the chip
+    int line;     // few columns: workgroups of a head's line (0: one for each column tile)
     unsigned size16, magic, magic_hi; // page_size / 16; the words of floor(2^32 / size16) + 1
     int tiles;    // column tiles: an upper bound over the batch
 };
 
 // Column tile `local` (R columns) of a sequence: its rows and positions, and
 // the cache tiles that some column sees: `sink_tiles` first ones, then
-// [first_tile, ...), n in all, in `splits` parts.
+// [first_tile, ...), n in all.
 struct TilePlan {
     SeqRows seq;
     int cols;         // columns of the sequence
     int pmin, pmax;   // positions of the tile's first and last row
     int span;         // positions that can have a slot
     int sink_tiles, first_tile, n;
-    int splits, per_split;
 };
 
-// Tiles of one sequence, roughly: for sharing out the splits.
-__device__ __forceinline__ int rough_tiles(const AttnArgs &a, int s)
+__device__ __forceinline__ TilePlan plan_tile(const AttnArgs &a, const SeqRows &seq, int local, int R)
 {
-    int64_t len = a.b.lengths[s];
-    const int64_t span = a.b.width * a.c.page_size;
-    len = len < 0 ? 0 : len > span ? span : len;
-    if (a.window) {
-        const int64_t seen = (int64_t)a.window + a.sinks + (a.b.row_start[s + 1] - a.b.row_start[s]);
-        len = seen < len && seen >= 0 ? seen : len;
-    }
-    return (int)((len + kTile - 1) / kTile);
-}
-
-// Cache tiles of one split: the batch's tiles over the workgroups wanted, at
-// least two per wave.  Every wave gets the same answer.
-__device__ __forceinline__ int split_tiles(const AttnArgs &a, int lane)
-{
-    float sum = 0.0f;
-    for (int s = lane; s < a.b.seqs; s += 64)
-        sum += (float)rough_tiles(a, s);
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1)
-        sum += __shfl_xor(sum, m, 64);
-    // each sequence has about tiles / seqs column tiles for every head
-    const float units = sum * (float)a.tiles / (float)a.b.seqs * (float)a.c.heads;
-    const int per = (int)(units / (float)a.wanted) + 1;
-    return __builtin_amdgcn_readfirstlane(per < 2 * kWaves ? 2 * kWaves : per);
-}
-
-__device__ __forceinline__ void plan_tile(const AttnArgs &a, int s, int local, int R, int lane, TilePlan &t)
-{
-    t.seq = seq_rows(a.b, s);
-    t.cols = t.seq.rows * a.group;
+    TilePlan t;
+    t.seq = seq;
+    t.cols = seq.rows * a.group;
     const int64_t c0 = (int64_t)local * R;
     const int64_t c1 = c0 + R < t.cols ? c0 + R : t.cols; // one past the last
     t.span = (int)(a.b.width * a.c.page_size);
-    t.pmin = (int)(t.seq.pos0 + c0 / a.group);
-    t.pmax = (int)(t.seq.pos0 + (c1 - 1) / a.group);
+    t.pmin = (int)(seq.pos0 + c0 / a.group);
+    t.pmax = (int)(seq.pos0 + (c1 - 1) / a.group);
     const int64_t end = (int64_t)t.pmax + 1;
     const int hi = end < 0 ? 0 : end > t.span ? t.span : (int)end;
     const int hi_tile = (hi + kTile - 1) / kTile;
@@ -133,16 +104,214 @@ __device__ __forceinline__ void plan_tile(const AttnArgs &a, int s, int local, i
             t.sink_tiles = t.first_tile = 0;
     }
     t.n = t.sink_tiles + hi_tile - t.first_tile;
-    t.splits = 1;
-    t.per_split = t.n;
-    if (a.splits > 1 && t.n > 0) {
-        const int per = split_tiles(a, lane);
-        const int want = (t.n + per - 1) / per;
-        t.splits = want < a.splits ? want : a.splits;
-        t.per_split = (t.n + t.splits - 1) / t.splits;
-        t.splits = (t.n + t.per_split - 1) / t.per_split;
-    }
+    return t;
 }
+
+// No column tile of a sequence of this length has more cache tiles.
+__device__ __forceinline__ int most_tiles(const AttnArgs &a, int64_t len, int R)
+{
+    const int64_t span = a.b.width * a.c.page_size;
+    len = len < 0 ? 0 : len > span ? span : len;
+    int64_t n = (len + kTile - 1) / kTile;
+    if (a.window) {
+        // the window of R / group + 1 rows ends inside a tile on either side
+        const int64_t w = ((int64_t)a.window + R / a.group + 1 + kTile - 1) / kTile + 1 + (a.sinks + kTile - 1) / kTile;
+        n = w < n ? w : n;
+    }
+    return (int)n;
+}
+
+// The work of one workgroup: cache tiles [begin, stop) of a column tile's
+// plan, and where its columns go: to the output (part < 0), or as rows part,
+// part + 1, ... of the partial results.
+struct Place {
+    int head, s, local;
+    TilePlan t;
+    int begin, stop;
+    int64_t part;
+};
+
+// The partial results of a column tile: part i starts at row base + i stride,
+// part 0 `extra` rows later.
+struct Parts {
+    int count;
+    int64_t base, stride, extra;
+};
+
+// Column tile -> sequence and its local number: the tiles of sequence s start
+// at row_start[s] group / R + s, which leaves it at least ceil(columns / R).
+// False: the sequence has no such tile.
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int R, int tile, int lane, Place &w)
+{
+    auto first_of = [&](int s) {
+        const int64_t r = a.b.row_start[s];
+        return (r < 0 ? 0 : r) * a.group / R + s;
+    };
+    w.s = wave_search((int)a.b.seqs, tile, lane, first_of);
+    const int64_t local = tile - first_of(w.s);
+    const SeqRows q = seq_rows(a.b, w.s);
+    if (local < 0 || local * R >= (int64_t)q.rows * a.group)
+        return false;
+    w.local = (int)local;
+    w.t = plan_tile(a, q, w.local, R);
+    return true;
+}
+
+// ---- many columns: a workgroup for each column tile, head and split -------
+// Cache tiles of one split: the batch's tiles over the workgroups wanted, at
+// least two per wave.  Every wave of both kernels gets the same answer.
+__device__ __forceinline__ int split_tiles(const AttnArgs &a, int R, int lane)
+{
+    float sum = 0.0f;
+    for (int s = lane; s < a.b.seqs; s += 64)
+        sum += (float)most_tiles(a, a.b.lengths[s], R);
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        sum += __shfl_xor(sum, m, 64);
+    // each sequence has about tiles / seqs column tiles for every head
+    const float units = sum * (float)a.tiles / (float)a.b.seqs * (float)a.c.heads;
+    const int per = (int)(units / (float)a.wanted) + 1;
+    return __builtin_amdgcn_readfirstlane(per < 2 * kWaves ? 2 * kWaves : per);
+}
+
+__device__ __forceinline__ Parts split_parts(const AttnArgs &a, int R, int tile, int head, int n, int lane,
+                                             int &per_split)
+{
+    Parts p{1, 0, 0, 0};
+    per_split = n;
+    if (a.splits > 1 && n > 0) {
+        const int per = split_tiles(a, R, lane);
+        const int want = (n + per - 1) / per;
+        p.count = want < a.splits ? want : a.splits;
+        per_split = (n + p.count - 1) / p.count;
+        p.count = (n + per_split - 1) / per_split;
+    }
+    p.base = ((int64_t)tile * a.c.heads + head) * R;
+    p.stride = (int64_t)a.tiles * a.c.heads * R;
+    return p;
+}
+
+// Workgroup -> (split, column tile, head), the head fastest: the eight XCDs
+// take workgroups in turn, so a head's cache stays in few L2s.  The last
+// column tiles, whose rows see most, start first.  False: nothing to do.
+__device__ __forceinline__ bool find_many(const AttnArgs &a, int R, int lane, Place &w)
+{
+    const int heads = (int)a.c.heads;
+    int id = (int)blockIdx.x;
+    w.head = id % heads;
+    id /= heads;
+    const int split = id % a.splits, tile = a.tiles - 1 - id / a.splits;
+    if (!find_tile(a, R, tile, lane, w))
+        return false;
+    int per = 0;
+    const Parts p = split_parts(a, R, tile, w.head, w.t.n, lane, per);
+    if (split >= p.count)
+        return false;
+    w.begin = split * per;
+    w.stop = w.begin + per < w.t.n ? w.begin + per : w.t.n;
+    w.part = p.count > 1 ? p.base + split * p.stride : -1;
+    return true;
+}
+
+// ---- few columns: equal shares of a line ----------------------------------
+// The cache tiles of all column tiles of all sequences, one after the other,
+// are cut into equal shares, one for each of a head's workgroups: a share ends
+// inside a column tile wherever it does, so lengths do not have to match for
+// the chip to be filled evenly.  A workgroup has at most one column tile that
+// began before its share and one that goes on after it, so it needs two
+// places for partial results: 2 p and 2 p + 1.  Where no sequence has more than
+// kWhole tiles, a column tile counts as one and is not cut.
+//
+// The arrays of the batch are read once, together, and kept in LDS.
+constexpr int kLineSeqs = 256;
+constexpr int kWhole = 12 * kWaves; // a join costs about as much as 12 tiles of a wave
+
+struct LineSeq {
+    int64_t at;            // where the sequence starts in the line
+    int first, rows, len;  // its rows
+    int per;               // tiles of one of its column tiles
+};
+
+struct Line {
+    const LineSeq *seq;
+    int64_t share, end;
+    int seqs, lane;
+    bool whole;
+
+    // Every wave of the workgroup takes part; each writes the same to `to`
+    // (whole groups of 64 sequences), which is read after the barrier here.
+    __device__ __forceinline__ void build(const AttnArgs &a, int R, int lane_, LineSeq *to)
+    {
+        seq = to;
+        seqs = (int)a.b.seqs;
+        lane = lane_;
+        LineSeq v[kLineSeqs / 64];
+        int most = 0;
+#pragma unroll
+        for (int k = 0; k < kLineSeqs / 64; ++k) {
+            const int s = 64 * k + lane;
+            v[k] = {0, 0, 0, 0, 0};
+            if (s < seqs) {
+                const int64_t b = a.b.row_start[s], e = a.b.row_start[s + 1];
+                v[k].len = a.b.lengths[s];
+                const bool ok = b >= 0 && b < e && e <= a.b.rows;
+                v[k].first = ok ? (int)b : 0;
+                v[k].rows = ok ? (int)(e - b) : 0;
+                const int n = most_tiles(a, v[k].len, R);
+                v[k].per = n < 1 ? 1 : n;
+                most = ok && v[k].per > most ? v[k].per : most;
+            }
+        }
+        whole = __builtin_amdgcn_ballot_w64(most > kWhole) == 0;
+        end = 0;
+#pragma unroll
+        for (int k = 0; k < kLineSeqs / 64; ++k) {
+            if (64 * k >= seqs)
+                continue;
+            if (whole)
+                v[k].per = 1;
+            const int64_t all = (((int64_t)v[k].rows * a.group + R - 1) / R) * v[k].per;
+            int64_t sum = all;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const int64_t up = __shfl_up(sum, m, 64);
+                sum += lane >= m ? up : 0;
+            }
+            v[k].at = end + sum - all;
+            end += __shfl(sum, 63, 64);
+            to[64 * k + lane] = v[k];
+        }
+        end = lane64(end);
+        share = (end + a.line - 1) / a.line;
+        const int64_t least = whole ? 1 : kWhole / 2;
+        share = share < least ? least : share;
+        __syncthreads();
+    }
+
+    static __device__ __forceinline__ int64_t lane64(int64_t v)
+    {
+        return (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)v) |
+                         (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+    }
+
+    // A sequence's entry, the same in all lanes.
+    __device__ __forceinline__ LineSeq of(int s) const
+    {
+        const LineSeq v = seq[s];
+        return {lane64(v.at), __builtin_amdgcn_readfirstlane(v.first), __builtin_amdgcn_readfirstlane(v.rows),
+                __builtin_amdgcn_readfirstlane(v.len), __builtin_amdgcn_readfirstlane(v.per)};
+    }
+
+    // The sequence that place x of the line belongs to: the last that starts
+    // there or before (an empty one starts where the next one does).
+    __device__ __forceinline__ int find(int64_t x) const
+    {
+        int n = 0;
+        for (int k = 0; 64 * k < seqs; ++k)
+            n += __popcll(__builtin_amdgcn_ballot_w64(64 * k + lane < seqs && seq[64 * k + lane].at <= x));
+        return n - 1;
+    }
+};
 
 // Largest of the four lane groups, in all of them.
 __device__ __forceinline__ float max_groups(float v)
@@ -164,43 +333,6 @@ __device__ __forceinline__ float sum_groups(float v)
 __device__ __forceinline__ unsigned pack_bf16(float a, float b)
 {
     return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){a, b}, bf16x2));
-}
-
-// The work of one workgroup.
-struct Place {
-    int head, split, s, local;
-    TilePlan t;
-    int begin, stop; // its share of the plan's cache tiles
-};
-
-// Workgroup id -> (split, column tile, head), the head fastest: the eight XCDs
-// take workgroups in turn, so a head's cache stays in few L2s.  The last
-// column tiles, whose rows see most, start first.  False: nothing to do.
-__device__ __forceinline__ bool find_work(const AttnArgs &a, int R, int id, int splits, int lane, Place &w)
-{
-    const int heads = (int)a.c.heads;
-    w.head = id % heads;
-    id /= heads;
-    w.split = id % splits;
-    const int tile = a.tiles - 1 - id / splits;
-    // the tiles of sequence s start at row_start[s] group / R + s, which leaves
-    // it at least ceil(columns / R)
-    auto first_of = [&](int s) {
-        const int64_t r = a.b.row_start[s];
-        return (r < 0 ? 0 : r) * a.group / R + s;
-    };
-    w.s = wave_search((int)a.b.seqs, tile, lane, first_of);
-    const int64_t local = tile - first_of(w.s);
-    const SeqRows q = seq_rows(a.b, w.s);
-    if (local < 0 || local * R >= (int64_t)q.rows * a.group)
-        return false;
-    w.local = (int)local;
-    plan_tile(a, w.s, w.local, R, lane, w.t);
-    if (w.split >= w.t.splits)
-        return false;
-    w.begin = w.split * w.t.per_split;
-    w.stop = w.begin + w.t.per_split < w.t.n ? w.begin + w.t.per_split : w.t.n;
-    return true;
 }
 
 // A wave's columns: queries, what each column sees, running sums.
@@ -342,18 +474,19 @@ __device__ __forceinline__ void spoil(f32x4 &acc, const f32x4 &count)
         acc[e] = count[e] > 0.0f ? __builtin_nanf("") : acc[e];
 }
 
-// Writes a column's result, or its part of it.  The lane's channels are [8 NB
+// Writes the columns' results, or their parts; col0: the wave's first column in the workgroup's tile.  The lane's channels are [8 NB
 // g, 8 NB (g + 1)): channel 2 NB e + j of them is acc[j][e].
 template <int NB, int kNQ>
-__device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w, const Columns<NB, kNQ> &q, int g)
+__device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w, const Columns<NB, kNQ> &q, int col0,
+                                              int c, int g)
 {
     constexpr int dim = 32 * NB;
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
         if (!q.live[n])
             continue;
-        if (w.t.splits > 1) {
-            const int64_t at = ((int64_t)w.split * a.b.rows + q.row[n]) * a.q_heads + q.qhead[n];
+        if (w.part >= 0) {
+            const int64_t at = w.part + col0 + n * 16 + c;
             if (g == 0)
                 *(f32x2 *)(a.part_ml + at * 2) = (f32x2){q.m[n], q.l[n]};
             float *o = a.part_o + at * dim + g * (8 * NB);
@@ -468,7 +601,6 @@ struct RawTile {
     unsigned ks[2][NB == 8 ? 2 : 1];
     unsigned v[8][kVW]; // k slots: positions 4g + i, 16 + 4g + i
     unsigned vs[2];
-    bool there[2];
 };
 
 // Codes of position c's channels [8 NB g, 8 NB (g + 1)) and their scales.
@@ -513,23 +645,6 @@ __device__ __forceinline__ void load_value(const uint8_t *src, unsigned (&v)[NB 
     }
 }
 
-template <int NB>
-__device__ __forceinline__ void load_tile(Pages<2> &pages, int i, int c, int g, RawTile<NB> &r)
-{
-    int page[2];
-    pages.take(page);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint64_t codes, scales;
-        r.there[h] = pages.at(i, h, page[h], 16 * NB, codes, scales);
-        load_keys<NB>(pages, codes, scales, c, g, r.k[h], r.ks[h]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            load_value<NB>(pages.vq + codes + (unsigned)((4 * g + k) * (NB * 16) + c * NB), r.v[4 * h + k]);
-        r.vs[h] = *(const unsigned *)(pages.vs + scales + (unsigned)((NB * c / 16) * pages.size + 4 * g));
-    }
-}
-
 // Byte b of a dword of codes -> the two channels as packed bf16.
 __device__ __forceinline__ unsigned cvt_byte(unsigned raw, float sc, int b)
 {
@@ -548,30 +663,129 @@ __device__ __forceinline__ unsigned even_of(unsigned w0, unsigned w1) { return _
 __device__ __forceinline__ unsigned odd_of(unsigned w0, unsigned w1) { return __builtin_amdgcn_perm(w1, w0, 0x07060302u); }
 
 // Few columns (NB = dim / 32; kNQ tiles of 16): every wave has the same
-// columns and takes every kWaves-th cache tile, straight from memory.
-template <int NB, int kNQ>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs a)
+// columns and takes every kW-th cache tile.  What bounds it is reading the
+// cache, so each wave keeps kD - 1 tiles in flight, loaded straight into LDS
+// (no registers, whole 16-byte pieces, 17 NB / 16 KB a tile) in the order in
+// which its lanes read them: the k-th 16-byte piece of a load goes to the
+// k-th place, so the order is chosen by the address that each lane loads
+// from.  A wave reads only what it loaded: no barrier.
+//
+// A stage: K pieces (half h, piece pc of a position, position c), V pieces
+// (h, i, g, piece) of position 4g + i, then dwords of scale bytes (K or V, h,
+// block, four positions).
+template <int NB>
+struct FewStage {
+    static constexpr int kPieces = 32 * NB;         // of K, and of V
+    static constexpr int kDwords = 16 * NB;         // of scales
+    static constexpr int kScalePad = kDwords < 64 ? 64 : kDwords;
+    static constexpr int kVAt = kPieces * 16, kSAt = 2 * kPieces * 16;
+    static constexpr int kBytes = kSAt + kScalePad * 4;
+    static constexpr int kLoads = 2 * kPieces / 64 + kScalePad / 64; // instructions of a tile
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+template <int NB>
+__device__ __forceinline__ void load_stage(const Pages<2> &pages, int i, const int (&page)[2], int lane,
+                                           unsigned char *st, bool (&there)[2])
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4;
+    using L = FewStage<NB>;
+    uint64_t codes[2], scales[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        there[h] = pages.at(i, h, page[h], 16 * NB, codes[h], scales[h]);
+#pragma unroll
+    for (int k = 0; k < L::kPieces / 64; ++k) {
+        const int u = 64 * k + lane, c = u % 16, pc = u / 16 % NB, h = u / (16 * NB);
+        __builtin_amdgcn_global_load_lds((global_void *)(pages.kq + (h ? codes[1] : codes[0]) + c * (16 * NB) + pc * 16),
+                                         (lds_void *)(st + k * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < L::kPieces / 64; ++k) {
+        const int u = 64 * k + lane, pc = u % NB, g = u / NB % 4, x = u / (4 * NB) % 4, h = u / (16 * NB);
+        __builtin_amdgcn_global_load_lds(
+            (global_void *)(pages.vq + (h ? codes[1] : codes[0]) + (4 * g + x) * (16 * NB) + pc * 16),
+            (lds_void *)(st + L::kVAt + k * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < L::kScalePad / 64; ++k) {
+        const int u = (64 * k + lane) % L::kDwords, t4 = u % 4, blk = u / 4 % NB, h = u / (4 * NB) % 2, v = u / (8 * NB);
+        __builtin_amdgcn_global_load_lds(
+            (global_void *)((v ? pages.vs : pages.ks) + (h ? scales[1] : scales[0]) + blk * pages.size + 4 * t4),
+            (lds_void *)(st + L::kSAt + k * 256), 4, 0, 0);
+    }
+}
+
+// A stage into the lane's registers.
+template <int NB>
+__device__ __forceinline__ void read_stage(const unsigned char *st, int c, int g, RawTile<NB> &r)
+{
+    using L = FewStage<NB>;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (NB == 2) {
+            const u32x2 w = *(const u32x2 *)(st + ((h * NB + g / 2) * 16 + c) * 16 + 8 * (g & 1));
+            r.k[h][0] = w[0];
+            r.k[h][1] = w[1];
+        } else {
+#pragma unroll
+            for (int e = 0; e < NB / 4; ++e) {
+                const u32x4 w = *(const u32x4 *)(st + ((h * NB + g * (NB / 4) + e) * 16 + c) * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    r.k[h][4 * e + j] = w[j];
+            }
+        }
+        const int blk = NB == 8 ? 2 * g : NB == 4 ? g : g >> 1;
+        r.ks[h][0] = st[L::kSAt + (h * NB + blk) * 16 + c];
+        if constexpr (NB == 8)
+            r.ks[h][1] = st[L::kSAt + (h * NB + blk + 1) * 16 + c];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            load_value<NB>(st + L::kVAt + (((h * 4 + x) * 4 + g) * (16 * NB) + c * NB), r.v[4 * h + x]);
+        r.vs[h] = *(const unsigned *)(st + L::kSAt + ((2 + h) * NB + NB * c / 16) * 16 + 4 * g);
+    }
+}
+
+// Bytes of LDS for the rings, or the join of the waves in the same place.
+template <int NB, int kNQ, int kW, int kD>
+__host__ __device__ constexpr int few_lds()
+{
+    constexpr int ring = kW * kD * FewStage<NB>::kBytes, join = kW * kNQ * (2 * NB * 64 * 16 + 2 * 16 * 4);
+    return ring > join ? ring : join;
+}
+
+// One workgroup's cache tiles of a column tile.
+template <int NB, int kNQ, int kW, int kD>
+__device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w, int lane, int wave,
+                                              unsigned char *lds)
+{
+    using L = FewStage<NB>;
     constexpr int R = 16 * kNQ;
-    Place w;
-    if (!find_work(a, R, (int)blockIdx.x, a.splits, lane, w))
-        return;
+    const int c = lane & 15, g = lane >> 4;
+    int i = w.begin + wave;
+    Pages<2> pages(a, w, lane, i, kW, 0);
+    unsigned char *ring = lds + wave * (kD * L::kBytes);
+    bool there[kD][2];
+    auto load = [&](int at, int z) {
+        int page[2];
+        pages.take(page);
+        load_stage<NB>(pages, at < w.stop ? at : w.stop - 1, page, lane, ring + z * L::kBytes, there[z]);
+    };
+    if (i < w.stop) {
+#pragma unroll
+        for (int z = 0; z < kD - 1; ++z)
+            load(i + z * kW, z);
+    }
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R, c, g, q);
-    int i = w.begin + wave;
-    Pages<2> pages(a, w, lane, i, kWaves, 0);
 
-    // codes one tile ahead
-    RawTile<NB> next;
-    if (i < w.stop)
-        load_tile<NB>(pages, i, c, g, next);
-    for (; i < w.stop; i += kWaves) {
-        RawTile<NB> r = next;
-        load_tile<NB>(pages, i + kWaves < w.stop ? i + kWaves : w.stop - 1, c, g, next);
-        const int j0 = pages.tile(i) * kTile;
-        const bool full = r.there[0] && r.there[1] && sees_all<NB, kNQ>(a, q, j0, w.t.span);
+    auto tile = [&](int at, const bool (&has)[2], const unsigned char *st) {
+        RawTile<NB> r;
+        read_stage<NB>(st, c, g, r);
+        const int j0 = pages.tile(at) * kTile;
+        const bool full = has[0] && has[1] && sees_all<NB, kNQ>(a, q, j0, w.t.span);
 
         f32x4 S[kNQ][2];
 #pragma unroll
@@ -595,14 +809,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
             vsb[k] = (r.vs[k >> 2] >> (8 * (k & 3))) & 0xFFu;
         unsigned nan_slots = 0, seen[kNQ];
         if (!full) {
-            mask_scores<NB, kNQ>(a, q, j0, w.t.span, r.there, g, S, seen);
+            mask_scores<NB, kNQ>(a, q, j0, w.t.span, has, g, S, seen);
             // positions that no column sees (past the last one, or never
             // written) are cleared: a weight of zero would not hide what they
             // hold.  NaN blocks are cleared too and counted below.
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int h = k >> 2, j = j0 + 16 * h + 4 * g + (k & 3);
-                const bool dead = j >= q.whi || !r.there[h];
+                const bool dead = j >= q.whi || !has[h];
                 const bool nan = vsb[k] == 0xFFu && !dead;
                 nan_slots |= (unsigned)nan << k;
                 if (dead || nan) {
@@ -646,31 +860,58 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
                     spoil(q.acc[n][j], count);
             }
         }
+    };
+
+    // s_waitcnt vmcnt: the loads of the kD - 1 younger tiles may be in flight
+    // (page numbers fetched in between only make it wait for more)
+    constexpr int kYounger = (kD - 1) * L::kLoads;
+    static_assert(kYounger < 64, "vmcnt has six bits");
+    constexpr unsigned kWait = 0x0F70u | (kYounger & 15) | ((kYounger >> 4) << 14);
+    while (i < w.stop) {
+#pragma unroll
+        for (int z = 0; z < kD; ++z) {
+            if (i >= w.stop)
+                break;
+            // the stage that was read last is loaded again: its reads were
+            // used in products, and nothing moves across the empty asm
+            asm volatile("" ::: "memory");
+            load(i + (kD - 1) * kW, (z + kD - 1) % kD);
+            __builtin_amdgcn_s_waitcnt(kWait);
+            asm volatile("" ::: "memory");
+            tile(i, there[z], ring + z * L::kBytes);
+            i += kW;
+        }
     }
 
-    // sums over the lane groups, then over the waves
-    __shared__ float sm[kWaves][kNQ][16], sl[kWaves][kNQ][16];
-    __shared__ f32x4 so[kWaves - 1][kNQ][2 * NB][64];
+    // sums over the lane groups, then over the waves, through the ring (after
+    // what is still in flight into it)
+    __builtin_amdgcn_s_waitcnt(0x0F70u);
+    f32x4 *so = (f32x4 *)lds;                               // [kW][kNQ][2 NB][64]
+    float *sm = (float *)(so + kW * kNQ * 2 * NB * 64);     // [kW][kNQ][16], and the sums after it
+    float *sl = sm + kW * kNQ * 16;
 #pragma unroll
-    for (int n = 0; n < kNQ; ++n) {
+    for (int n = 0; n < kNQ; ++n)
         q.l[n] = sum_groups(q.l[n]);
-        if (g == 0) {
-            sm[wave][n][c] = q.m[n];
-            sl[wave][n][c] = q.l[n];
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int n = 0; n < kNQ; ++n) {
+            sm[(wave * kNQ + n) * 16 + c] = q.m[n];
+            sl[(wave * kNQ + n) * 16 + c] = q.l[n];
         }
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
-        float up = sm[0][n][c];
+        float up = sm[n * 16 + c];
 #pragma unroll
-        for (int x = 1; x < kWaves; ++x)
-            up = __builtin_fmaxf(up, sm[x][n][c]);
+        for (int x = 1; x < kW; ++x)
+            up = vmax(up, sm[(x * kNQ + n) * 16 + c]);
         float sum = 0.0f;
 #pragma unroll
-        for (int x = 0; x < kWaves; ++x) {
-            const float mx = sm[x][n][c];
-            sum += sl[x][n][c] * (mx == up ? 1.0f : __builtin_amdgcn_exp2f(mx - up));
+        for (int x = 0; x < kW; ++x) {
+            const float mx = sm[(x * kNQ + n) * 16 + c];
+            sum += sl[(x * kNQ + n) * 16 + c] * (mx == up ? 1.0f : __builtin_amdgcn_exp2f(mx - up));
         }
         const float f = q.m[n] == up ? 1.0f : __builtin_amdgcn_exp2f(q.m[n] - up);
         q.m[n] = up;
@@ -679,20 +920,63 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_few_kernel(AttnArgs 
         for (int j = 0; j < 2 * NB; ++j) {
             q.acc[n][j] *= f;
             if (wave)
-                so[wave - 1][n][j][lane] = q.acc[n][j];
+                so[((wave * kNQ + n) * 2 * NB + j) * 64 + lane] = q.acc[n][j];
         }
     }
     __syncthreads();
     if (wave)
-        return;
+        return; // to the caller's barrier
 #pragma unroll
     for (int n = 0; n < kNQ; ++n)
 #pragma unroll
         for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-            for (int x = 0; x < kWaves - 1; ++x)
-                q.acc[n][j] += so[x][n][j][lane];
-    store_columns<NB, kNQ>(a, w, q, g);
+            for (int x = 1; x < kW; ++x)
+                q.acc[n][j] += so[((x * kNQ + n) * 2 * NB + j) * 64 + lane];
+    store_columns<NB, kNQ>(a, w, q, 0, c, g);
+}
+
+template <int NB, int kNQ, int kW, int kD>
+__global__ __launch_bounds__(64 * kW, 2) void attention_few_kernel(AttnArgs a)
+{
+    constexpr int R = 16 * kNQ;
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int heads = (int)a.c.heads, p = (int)blockIdx.x / heads;
+    Place w;
+    w.head = (int)blockIdx.x % heads;
+    if (a.line == 0) { // more sequences than a line holds: a column tile each
+        if (!find_tile(a, R, a.tiles - 1 - p, lane, w))
+            return;
+        w.begin = 0;
+        w.stop = w.t.n;
+        w.part = -1;
+    }
+    Line line;
+    int64_t begin = 0, end = 1;
+    if (a.line) {
+        line.build(a, R, lane, (LineSeq *)(lds + few_lds<NB, kNQ, kW, kD>()));
+        begin = p * line.share;
+        end = begin + line.share < line.end ? begin + line.share : line.end;
+    }
+    for (int64_t x = begin; x < end;) {
+        int64_t next = end;
+        if (a.line) {
+            w.s = line.find(x);
+            const LineSeq q = line.of(w.s);
+            w.local = (int)((x - q.at) / q.per);
+            const int64_t tile = q.at + (int64_t)w.local * q.per; // the column tile's first place in the line
+            next = tile + q.per < end ? tile + q.per : end;
+            w.t = plan_tile(a, {q.first, q.rows, (int64_t)q.len - q.rows}, w.local, R);
+            w.begin = line.whole ? 0 : (int)(x - tile) < w.t.n ? (int)(x - tile) : w.t.n;
+            w.stop = line.whole ? w.t.n : (int)(next - tile) < w.t.n ? (int)(next - tile) : w.t.n;
+            const bool all = x == tile && next == tile + q.per;
+            w.part = all ? -1 : ((int64_t)(2 * p + (tile >= begin ? 1 : 0)) * heads + w.head) * R;
+        }
+        attention_few<NB, kNQ, kW, kD>(a, w, lane, wave, lds);
+        x = next;
+        __syncthreads(); // the join is done with the ring
+    }
 }
 
 // Many columns: the waves have columns of their own and share the cache tiles
@@ -718,7 +1002,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     extern __shared__ __align__(16) unsigned char lds[];
     WideStage<NB> *stage = (WideStage<NB> *)lds;
     Place w;
-    if (!find_work(a, R, (int)blockIdx.x, a.splits, lane, w))
+    if (!find_many(a, R, lane, w))
         return;
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R + wave * kNQ * 16, c, g, q);
@@ -864,7 +1148,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
     for (int n = 0; n < kNQ; ++n)
         q.l[n] = sum_groups(q.l[n]);
-    store_columns<NB, kNQ>(a, w, q, g);
+    store_columns<NB, kNQ>(a, w, q, wave * kNQ * 16, c, g);
 }
 
 // Joins the splits of the column tiles that have several: `per_tile`
@@ -877,27 +1161,53 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, 
     constexpr int dim = 32 * NB, along = dim / 4;
     __shared__ f32x4 so[256];
     __shared__ float sl[256];
+    __shared__ LineSeq seqs[kLineSeqs];
     const int lane = threadIdx.x & 63;
     const int part = (int)(blockIdx.x % (unsigned)per_tile);
+    const int id = (int)(blockIdx.x / (unsigned)per_tile), tile = id / (int)a.c.heads;
     Place w;
-    if (!find_work(a, R, (int)(blockIdx.x / (unsigned)per_tile), 1, lane, w) || w.t.splits == 1)
+    w.head = id % (int)a.c.heads;
+    if (!find_tile(a, R, tile, lane, w))
         return;
+    Parts parts;
+    if (a.line) {
+        Line line;
+        line.build(a, R, lane, seqs);
+        const LineSeq q = line.of(w.s);
+        const int64_t start = q.at + (int64_t)w.local * q.per;
+        const int64_t p0 = start / line.share, p1 = (start + q.per - 1) / line.share;
+        parts.count = (int)(p1 - p0) + 1;
+        parts.stride = 2 * a.c.heads * R;
+        parts.extra = a.c.heads * R;
+        parts.base = (2 * p0 * a.c.heads + w.head) * R;
+    } else {
+        int per = 0;
+        parts = split_parts(a, R, tile, w.head, w.t.n, lane, per);
+    }
+    if (parts.count == 1)
+        return;
+    auto part_at = [&](int i) { return parts.base + i * parts.stride + (i == 0 ? parts.extra : 0); };
     const int ways = 256 / along / cols; // threads along the splits
     const int d4 = threadIdx.x % along, way = threadIdx.x / along % ways, sub = threadIdx.x / along / ways;
     const int stop = (w.local + 1) * R < w.t.cols ? (w.local + 1) * R : w.t.cols;
-    const int64_t step = a.b.rows * a.q_heads;
     for (int col0 = w.local * R + part * cols; col0 < stop; col0 += per_tile * cols) {
         const int col = col0 + sub < stop ? col0 + sub : stop - 1;
         const int i = col / a.group, row = w.t.seq.first + i, head = w.head * a.group + col - i * a.group;
-        const int64_t at = (int64_t)row * a.q_heads + head;
+        const int at = col - w.local * R;
         f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
         float l = 0.0f, m = -__builtin_inff();
-        for (int x = 0; x < w.t.splits; ++x)
-            m = vmax(m, a.part_ml[(at + x * step) * 2]);
-        for (int x = way; x < w.t.splits; x += ways) {
-            const f32x2 ml = *(const f32x2 *)(a.part_ml + (at + x * step) * 2);
+        for (int x = way; x < parts.count; x += ways)
+            m = vmax(m, a.part_ml[(part_at(x) + at) * 2]);
+        sl[threadIdx.x] = m;
+        __syncthreads();
+        for (int x = 0; x < ways; ++x)
+            m = vmax(m, sl[(sub * ways + x) * along + d4]);
+        __syncthreads();
+        for (int x = way; x < parts.count; x += ways) {
+            const int64_t r = part_at(x) + at;
+            const f32x2 ml = *(const f32x2 *)(a.part_ml + r * 2);
             const float f = ml[0] == m ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - m);
-            o += f * *(const f32x4 *)(a.part_o + (at + x * step) * dim + d4 * 4);
+            o += f * *(const f32x4 *)(a.part_o + r * dim + d4 * 4);
             l += f * ml[1];
         }
         so[threadIdx.x] = o;
@@ -916,11 +1226,31 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, 
     }
 }
 
-// Columns of a workgroup, and how its waves share them.
+// Stages of a wave's ring, few columns.
+constexpr int few_depth(int64_t dim) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
+
+// Bytes of the line's table in LDS.
+constexpr int line_lds(int64_t seqs) { return (int)((seqs + 63) / 64 * 64) * (int)sizeof(LineSeq); }
+
+// Workgroups of attention_few_kernel that a CU holds: by registers three with
+// one column tile (dim 64, 128), else two; by LDS as computed.
+int few_resident(int64_t dim, int nq, int64_t seqs)
+{
+    const int ring = dim == 64    ? few_lds<2, 1, kWaves, few_depth(64)>()
+                     : dim == 128 ? few_lds<4, 1, kWaves, few_depth(128)>()
+                                  : few_lds<8, 1, kWaves, few_depth(256)>();
+    const int lds = 160 * 1024 / (ring + line_lds(seqs)), regs = nq == 1 && dim < 256 ? 3 : 2;
+    return lds < regs ? lds : regs;
+}
+
+// Columns of a workgroup, and how the work is cut.
 struct Shape {
     bool many;
     int nq, R;
-    int tiles, splits, wanted;
+    int tiles, wanted;
+    int splits; // many columns
+    int line;   // few columns
+    int64_t parts; // rows of partial results (0: none, and no join)
 };
 
 Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t window, int64_t sinks)
@@ -932,29 +1262,57 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
     s.nq = mean <= 16 || c.dim == 256 ? 1 : 2;
     s.R = 16 * s.nq * (s.many ? kWaves : 1);
     s.tiles = (int)(cols / s.R + b.seqs);
-    // workgroups that are resident together: few columns by registers, many by LDS
-    s.wanted = (s.many ? (c.dim == 64 ? 4 : c.dim == 128 ? 2 : 1) : 4) * device_cus();
     s.splits = 1;
     const int64_t groups = (int64_t)s.tiles * c.heads;
-    if (b.seqs <= kSplitSeqs && 2 * groups <= s.wanted) {
-        // tiles of the longest sequence the table can hold
-        int64_t span = b.width * c.page_size;
-        if (window && window + sinks + b.rows < span)
-            span = window + sinks + b.rows;
-        const int64_t most = (span / kTile + 2 * kWaves) / (2 * kWaves);
-        // twice the mean: the longer sequences of a mixed batch take more
-        int64_t n = 2 * (s.wanted / groups);
-        n = n < most ? n : most;
-        s.splits = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+    // cache tiles of the longest sequence the table can hold
+    int64_t span = b.width * c.page_size;
+    if (window && window + sinks + b.rows + 2 * kTile < span)
+        span = window + sinks + b.rows + 2 * kTile;
+    const int64_t most = (span + kTile - 1) / kTile;
+    if (s.many) {
+        // resident workgroups, by LDS
+        s.wanted = (c.dim == 64 ? 4 : c.dim == 128 ? 2 : 1) * device_cus();
+        if (b.seqs <= kLineSeqs && 2 * groups <= s.wanted) {
+            const int64_t cut = (most + 2 * kWaves - 1) / (2 * kWaves);
+            // twice the mean: the longer sequences of a mixed batch take more
+            int64_t n = 2 * (s.wanted / groups);
+            n = n < cut ? n : cut;
+            s.splits = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+        }
+        s.parts = s.splits > 1 ? (int64_t)s.splits * groups * s.R : 0;
+    } else {
+        s.wanted = (b.seqs <= kLineSeqs ? few_resident(c.dim, s.nq, b.seqs) : 2) * device_cus();
+        // With many column tiles the chip evens out by itself
+        if (b.seqs <= kLineSeqs && groups <= 4 * s.wanted) {
+            s.line = (int)((s.wanted + c.heads - 1) / c.heads);
+            // uncut column tiles take a workgroup each: no fewer than there are tiles
+            if (most <= kWhole)
+                s.line = s.tiles;
+            else
+                s.parts = 2 * (int64_t)s.line * c.heads * s.R;
+        }
     }
     return s;
+}
+
+template <int NB, int kNQ, int kW, int kD>
+hipError_t launch_few(const AttnArgs &a, int64_t grid, hipStream_t stream)
+{
+    constexpr int most = few_lds<NB, kNQ, kW, kD>() + kLineSeqs * (int)sizeof(LineSeq);
+    static_assert(most <= 160 * 1024, "LDS of a CU");
+    const hipError_t e = allow_dynamic_lds((const void *)attention_few_kernel<NB, kNQ, kW, kD>, most);
+    if (e != hipSuccess)
+        return e;
+    const int bytes = few_lds<NB, kNQ, kW, kD>() + line_lds(a.line ? a.b.seqs : 0);
+    attention_few_kernel<NB, kNQ, kW, kD><<<dim3((unsigned)grid), dim3(64 * kW), bytes, stream>>>(a);
+    return hipGetLastError();
 }
 
 template <int NB>
 hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
 {
-    const int64_t grid = (int64_t)s.tiles * s.splits * a.c.heads;
-    if (grid > 0x7FFFFFFF || a.b.rows * a.q_heads > 0x7FFFFFFF)
+    const int64_t grid = (s.line ? (int64_t)s.line : (int64_t)s.tiles * s.splits) * a.c.heads;
+    if (grid > 0x7FFFFFFF)
         return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), w(64 * kWaves);
     constexpr int kMost = NB == 8 ? 1 : 2; // column tiles a wave has registers for
@@ -965,18 +1323,23 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
         if (e != hipSuccess)
             return e;
         attention_many_kernel<NB, kMost><<<g, w, bytes, stream>>>(a);
-    } else if (s.nq > 1) {
-        attention_few_kernel<NB, kMost><<<g, w, 0, stream>>>(a);
     } else {
-        attention_few_kernel<NB, 1><<<g, w, 0, stream>>>(a);
+        hipError_t e;
+        if (s.nq > 1)
+            e = launch_few<NB, kMost, kWaves, few_depth(32 * NB)>(a, grid, stream);
+        else
+            e = launch_few<NB, 1, kWaves, few_depth(32 * NB)>(a, grid, stream);
+        if (e != hipSuccess)
+            return e;
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || s.splits == 1)
+    if (e != hipSuccess || s.parts == 0)
         return e;
     // about 2048 workgroups (8 a CU), each with the columns abreast that leave
-    // a thread for every split
+    // threads for four parts or more
+    const int parts = s.line ? s.line : s.splits;
     int cols = 256 / (8 * NB);
-    while (cols > 1 && 256 / (8 * NB) / cols < s.splits)
+    while (cols > 1 && 256 / (8 * NB) / cols < (parts < 4 ? parts : 4))
         cols /= 2;
     const int64_t groups = (int64_t)s.tiles * a.c.heads, chunks = (s.R + cols - 1) / cols;
     int64_t per = 2048 / groups;
@@ -989,8 +1352,7 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
 
 int64_t attention_workspace(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t window, int64_t sinks)
 {
-    const Shape s = shape_of(q_heads, c, b, window, sinks);
-    return s.splits == 1 ? 0 : (int64_t)s.splits * b.rows * q_heads * (c.dim + 2) * 4;
+    return shape_of(q_heads, c, b, window, sinks).parts * (c.dim + 2) * 4;
 }
 
 hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q_heads, const mx_cache &c,
@@ -1002,7 +1364,7 @@ hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q
     a.q = q;
     a.out = out;
     a.part_o = (float *)workspace;
-    a.part_ml = a.part_o + (int64_t)s.splits * b.rows * q_heads * c.dim;
+    a.part_ml = a.part_o + s.parts * c.dim;
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.c = c;
@@ -1013,6 +1375,7 @@ hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q
     a.sinks = (int)sinks;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     a.splits = s.splits;
+    a.line = s.line;
     a.wanted = s.wanted;
     a.size16 = (unsigned)(c.page_size / 16);
     const uint64_t magic = ((uint64_t)1 << 32) / a.size16 + 1;

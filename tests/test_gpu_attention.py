@@ -261,6 +261,30 @@ def test_graph_decodes_a_growing_sequence(K):
     compare(out, want, room)
 
 
+@pytest.mark.parametrize("dim,q_heads,heads", [(64, 2, 2), (128, 4, 1), (256, 3, 1), (128, 24, 1)])
+def test_shares_end_anywhere(K, dim, q_heads, heads):
+    """Sequences of very different lengths, short and empty ones among long
+    ones: the equal shares of the work then begin and end inside them."""
+    say(f"[attention shares] dim={dim} heads={q_heads}/{heads}")
+    rng = np.random.default_rng(21)
+    new = [1, 1, 1, 2, 0, 1, 3, 1, 1, 1, 2, 1]
+    lengths = [3000, 5, 0, 1700, 40, 2200, 64, 3100, 1, 1601, 2, 1537]
+    s = Setup(rng, new, lengths, q_heads, heads, dim, 128)
+    s.check(K)
+    s.check(K, window=1800, sinks=70)
+    s.check(K, window=300, sinks=5)
+
+
+def test_more_sequences_than_a_line(K):
+    # long sequences, and one more of them than the shares are made for
+    say("[attention 257 sequences]")
+    rng = np.random.default_rng(22)
+    new = [1] * 257
+    lengths = [1 + (37 * i) % 90 for i in range(256)] + [2100]
+    Setup(rng, new, lengths, 2, 1, 64, 64).check(K)
+    Setup(rng, new[1:], lengths[1:], 2, 1, 64, 64).check(K)
+
+
 def test_many_sequences(K):
     say("[attention many]")
     rng = np.random.default_rng(17)
