@@ -283,7 +283,7 @@ struct Line {
         }
         end = lane64(end);
         share = (end + a.line - 1) / a.line;
-        const int64_t least = whole ? 1 : kWhole / 2;
+        const int64_t least = whole ? 1 : 2 * kWaves;
         share = share < least ? least : share;
         __syncthreads();
     }
@@ -1282,14 +1282,10 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
         s.parts = s.splits > 1 ? (int64_t)s.splits * groups * s.R : 0;
     } else {
         s.wanted = (b.seqs <= kLineSeqs ? few_resident(c.dim, s.nq, b.seqs) : 2) * device_cus();
-        // With many column tiles the chip evens out by itself
-        if (b.seqs <= kLineSeqs && groups <= 4 * s.wanted) {
+        // with many column tiles the chip evens out by itself
+        if (b.seqs <= kLineSeqs && groups <= 4 * s.wanted && most > kWhole) {
             s.line = (int)((s.wanted + c.heads - 1) / c.heads);
-            // uncut column tiles take a workgroup each: no fewer than there are tiles
-            if (most <= kWhole)
-                s.line = s.tiles;
-            else
-                s.parts = 2 * (int64_t)s.line * c.heads * s.R;
+            s.parts = 2 * (int64_t)s.line * c.heads * s.R;
         }
     }
     return s;
@@ -1325,10 +1321,9 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
         attention_many_kernel<NB, kMost><<<g, w, bytes, stream>>>(a);
     } else {
         hipError_t e;
-        if (s.nq > 1)
-            e = launch_few<NB, kMost, kWaves, few_depth(32 * NB)>(a, grid, stream);
-        else
-            e = launch_few<NB, 1, kWaves, few_depth(32 * NB)>(a, grid, stream);
+        constexpr int kD = few_depth(32 * NB);
+        e = s.nq > 1 ? launch_few<NB, kMost, kWaves, kD>(a, grid, stream)
+                     : launch_few<NB, 1, kWaves, kD>(a, grid, stream);
         if (e != hipSuccess)
             return e;
     }
