@@ -507,14 +507,24 @@ def _gpu(t, dtype, name):
 
 def _gpu_bf16(t, name):
     """Address of a contiguous GPU tensor of bf16 values (or their bits)."""
-    return _gpu(t, t.dtype if t.dtype in _bf16_types() else _torch().bfloat16, name)
+    if t.dtype in _bf16_types() and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, _bf16_types(), name)
 
 
-def _call(fn, where, stream, tensors, *args):
-    """fn(*args, stream) with the tensors' device current (they share one)."""
-    torch = _torch()
-    dev = tensors[0].get_device()
-    if torch._C._cuda_getDeviceCount() > 1:
+_one_device = None
+
+
+def _on_device(where, stream, tensors):
+    """(the current device is the tensors' one, their device, stream handle)
+    of tensors that have to share a device."""
+    global _one_device
+    torch = _torch_module
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    dev = 0
+    if not _one_device:
+        dev = tensors[0].get_device()
         for t in tensors:
             if t.get_device() != dev:
                 raise ValueError(f"{where}: tensors lie on cuda:{dev} and {t.device}")
@@ -524,10 +534,16 @@ def _call(fn, where, stream, tensors, *args):
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
     else:
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    return _one_device or torch._C._cuda_getDevice() == dev, dev, stream
+
+
+def _call(fn, where, stream, tensors, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    here, dev, stream = _on_device(where, stream, tensors)
+    if here:
         st = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _torch_module.cuda.device(dev):
             st = fn(*args, stream)
     if st:
         raise KQError(st, where)
@@ -582,14 +598,18 @@ def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
     if qw.shape != (N, K // 2) or sw.shape != (N, K // 32):
         raise ValueError("operand shapes do not match")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=x.device)
-    elif out.shape != (M, N):
-        raise ValueError("out must be float32 or bfloat16 [M, N]")
-    if out.dtype not in (torch.float32, torch.bfloat16) or out.dtype is not (out_dtype or out.dtype):
-        raise ValueError(f"out is {out.dtype}: float32 or bfloat16, as out_dtype says")
+        dtype = out_dtype or torch.float32
+        out = x.new_empty((M, N), dtype=dtype)
+    else:
+        dtype = out.dtype
+        if out.shape != (M, N) or dtype is not (out_dtype or dtype):
+            raise ValueError("out must be float32 or bfloat16 [M, N], as out_dtype says")
+    bf16 = dtype is torch.bfloat16
+    if not bf16 and dtype is not torch.float32:
+        raise ValueError(f"out is {dtype}: float32 or bfloat16 is wanted")
     u8 = torch.uint8
     _call(_lib.mx_gemv, "mx_gemv", stream, (x, qw, sw, out), _gpu_bf16(x, "x"), M, _gpu(qw, u8, "qw"),
-          _gpu(sw, u8, "sw"), N, K, _gpu(out, out.dtype, "out"), 1 if out.dtype is torch.bfloat16 else 0)
+          _gpu(sw, u8, "sw"), N, K, _gpu(out, dtype, "out"), bf16)
     return out
 
 
@@ -667,7 +687,7 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
     rows, heads, _ = q.shape
     qp, qst = _heads_view(q, "q", heads, dim)
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((rows, heads, dim), dtype=torch.bfloat16)
         op, ost = out.data_ptr(), heads * dim
     else:
         if out.shape[0] != rows:
@@ -677,14 +697,15 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
     tensors = (q, out, *cache, page_table, row_start, lengths)
     if workspace is None:
         # the size goes by the compute units of the current device: the tensors' one
-        if torch._C._cuda_getDevice() == q.get_device():
+        here, dev, _ = _on_device("mx_cache_attention", stream, tensors)
+        if here:
             need = _attention_bytes(heads, c, b, window, sinks)
         else:
-            with torch.cuda.device(q.device):
+            with torch.cuda.device(dev):
                 need = _attention_bytes(heads, c, b, window, sinks)
         wp = 0
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     else:
         need = workspace.numel()
         tensors += (workspace,)

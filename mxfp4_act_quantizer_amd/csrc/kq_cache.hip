@@ -9,7 +9,7 @@
 // rotated key gets exactly the codes that the butterfly kq_quantize gives it.
 //
 // A wave keeps its 16 blocks of a row (or all blocks of 16 / blocks rows, where
-// a row has fewer) and goes through up to eight steps of rows with them: the
+// a row has fewer) and goes through up to four steps of rows with them: the
 // factors of a block are read once, the bf16 side is whole runs of 1 KB, and
 // the loads of all steps are in flight together.  The rows' slots are found by
 // the lanes side by side, before the steps.
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWaves = 4;
 
-constexpr int kSteps = 8;
+constexpr int kSteps = 4; // 1, 2, 4, 8, 12: 25.6, 20.2, 19.4, 19.0, 20.9 us (9224 rotated rows), 3.8 .. 4.5 us (61)
 constexpr unsigned kXcds = 8;
 
 // How a wave's quads lie over rows and blocks.
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_cache_read_kernel(mx_cache c, 
                 __builtin_bit_cast(u32x4, mx_bf16x8(w[i], scale_operand(s[i])));
 }
 
-// Eight steps a wave where that leaves four waves a CU; fewer rows are spread
+// Four steps a wave where that leaves four waves a CU; fewer rows are spread
 // over more waves.
 Tiling tiling(const mx_cache &c, const mx_batch &b)
 {
