@@ -872,8 +872,9 @@ __device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w,
         for (int z = 0; z < kD; ++z) {
             if (i >= w.stop)
                 break;
-            // the stage that was read last is loaded again: its reads were
-            // used in products, and nothing moves across the empty asm
+            // the stage that was read last is loaded again, once its reads have
+            // arrived; nothing moves across the empty asm
+            __builtin_amdgcn_s_waitcnt(0xC07Fu); // lgkmcnt(0) alone
             asm volatile("" ::: "memory");
             load(i + (kD - 1) * kW, (z + kD - 1) % kD);
             __builtin_amdgcn_s_waitcnt(kWait);
