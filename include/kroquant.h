@@ -378,11 +378,13 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *batch, uint16_t *k, uin
  *   q_heads    a multiple of heads, at most 4096; rows * q_heads < 2^31
  *   scale      1e-30 .. 1e30 (usually 1 / sqrt(dim))
  *   window     0 (none) .. 2^30;  sinks  0 .. 2^30, ignored without a window
- *   out        dev, bf16, as q with out_stride
+ *   out        dev, bf16, as q with out_stride; from its first to its last
+ *              byte it may not overlap an input (slices of q's own buffer do)
  *   workspace  dev, 16-byte aligned, workspace_bytes of it: at least what
  *              mx_cache_attention_workspace gives for the same arguments
- *              (which may be 0: NULL is then allowed); overwritten.  Calls
- *              that overlap in time need one each.
+ *              (which may be 0: NULL is then allowed; too few are
+ *              KQ_ERR_ARG); overwritten.  Calls that overlap in time need one
+ *              each, and so do graphs whose replays may.
  * dim is 64, 128 or 256 here.  One or two launches on `stream`.  rows == 0 or
  * seqs == 0 is a no-op.
  */

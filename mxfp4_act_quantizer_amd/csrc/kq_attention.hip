@@ -253,7 +253,7 @@ struct Line {
             v[k] = {0, 0, 0, 0, 0};
             if (s < seqs) {
                 const int64_t b = a.b.row_start[s], e = a.b.row_start[s + 1];
-                v[k].len = a.b.lengths[s];
+                v[k].len = a.b.lengths[s] < 0 ? 0 : a.b.lengths[s];
                 const bool ok = b >= 0 && b < e && e <= a.b.rows;
                 v[k].first = ok ? (int)b : 0;
                 v[k].rows = ok ? (int)(e - b) : 0;

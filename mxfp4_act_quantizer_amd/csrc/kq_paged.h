@@ -37,7 +37,8 @@ __device__ __forceinline__ int wave_search(int S, int64_t t, int lane, Key key)
 }
 
 // Rows [first, first + rows) of the batch belong to the sequence; the i-th
-// is position pos0 + i.
+// is position pos0 + i.  (A negative length is taken as 0: either way every
+// position is negative, and positions then fit 32 bits.)
 struct SeqRows {
     int first, rows;
     int64_t pos0;
@@ -50,7 +51,8 @@ __device__ __forceinline__ SeqRows seq_rows(const mx_batch &b, int s)
     const bool ok = a >= 0 && a < e && e <= b.rows;
     r.first = ok ? (int)a : 0;
     r.rows = ok ? (int)(e - a) : 0;
-    r.pos0 = (int64_t)b.lengths[s] - (e - a);
+    const int length = b.lengths[s];
+    r.pos0 = (int64_t)(length < 0 ? 0 : length) - (e - a);
     return r;
 }
 

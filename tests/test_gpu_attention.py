@@ -172,6 +172,24 @@ def test_rows_that_see_nothing(K):
     assert (K.mx_cache_attention(s.q.cuda(), c, table[:, :0].contiguous(), start, lengths) == 0).all()
 
 
+@pytest.mark.parametrize("rows", [1, 3])
+def test_extreme_lengths(K, rows):
+    """The smallest and largest 32-bit lengths, and lengths just below and
+    above zero: negative positions see nothing, positions far past the table
+    see all of it."""
+    say(f"[attention extreme lengths] rows={rows}")
+    rng = np.random.default_rng(23)
+    s = Setup(rng, [rows] * 6, [64] * 6, 4, 2, 64, 16)
+    s.lengths[:] = [-2 ** 31, -2 ** 31 + 1, -1, 0, 2 ** 31 - 1, 64]
+    s.table[:] = s.table[4]  # positions past a length must not matter: every page is one of sequence 4's
+    want, _ = s.want()
+    assert (want[:4 * rows] == 0).all() and (want[4 * rows:] != 0).any()
+    got = s.check(K)
+    assert (got[:4 * rows] == 0).all()
+    s.check(K, window=30, sinks=2)
+    s.check(K, window=1 << 30, sinks=1 << 30)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_nan_stays_where_it_is_seen(K, dim):
     """NaN blocks in keys and values, a NaN and an infinity in q: only rows

@@ -178,6 +178,22 @@ def test_rows_without_a_slot(K):
             np.testing.assert_array_equal(got[r].float().cpu().numpy(), w)
 
 
+def test_extreme_lengths(K):
+    # positions at the ends of 32 bits have no slot: nothing is written, nothing read
+    say("[cache extreme lengths]")
+    rng = np.random.default_rng(6)
+    want = garbage(rng, 4, 2, 16, 64)
+    cache = K.MXCache(*(dev(a) for a in want))
+    kt, _ = rows_bf16(rng, 8, 2, 64)
+    args = (i32([[0, 1]] * 4), i32([0, 2, 4, 6, 8]), i32([-2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1, -1]))
+    K.mx_cache_write(kt.cuda(), kt.cuda(), cache, *args)
+    for got, w in zip(cache, want):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
+    k = torch.full((8, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    K.mx_cache_read(cache, *args, k=k, v=k.clone())
+    assert (k == 3).all()
+
+
 def test_many_sequences(K):
     # more sequences than one and two rounds of the search cover, empty ones among them
     say("[cache many]")
