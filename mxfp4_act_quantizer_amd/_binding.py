@@ -549,10 +549,20 @@ def _call(fn, where, stream, tensors, *args):
         raise KQError(st, where)
 
 
+def _new(like, shape, dtype, stream):
+    """An empty tensor on like's device that belongs to the call's stream: one
+    of the current stream's could be given to that stream's next work, or still
+    be in its earlier work's hands, while the call writes it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _torch_module.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _heads_view(t, name, heads, dim):
     """Address and row stride of a bf16 [rows, heads, dim] view whose rows are
     dense inside and any 16-byte multiple apart."""
-    if not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a torch tensor on the GPU")
     if t.dtype not in _bf16_types():
         raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
@@ -599,7 +609,7 @@ def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
         raise ValueError("operand shapes do not match")
     if out is None:
         dtype = out_dtype or torch.float32
-        out = x.new_empty((M, N), dtype=dtype)
+        out = _new(x, (M, N), dtype, stream)
     else:
         dtype = out.dtype
         if out.shape != (M, N) or dtype is not (out_dtype or dtype):
@@ -644,9 +654,9 @@ def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=No
         rows = k.shape[0]
     shape = (int(rows), heads, dim)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.kq.device)
+        k = _new(cache.kq, shape, torch.bfloat16, stream)
     if v is None:
-        v = torch.empty_like(k)
+        v = _new(cache.kq, shape, torch.bfloat16, stream)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {list(shape)}")
     b = _batch_arg(page_table, row_start, lengths, shape[0])
@@ -687,7 +697,7 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
     rows, heads, _ = q.shape
     qp, qst = _heads_view(q, "q", heads, dim)
     if out is None:
-        out = q.new_empty((rows, heads, dim), dtype=torch.bfloat16)
+        out = _new(q, (rows, heads, dim), torch.bfloat16, stream)
         op, ost = out.data_ptr(), heads * dim
     else:
         if out.shape[0] != rows:
@@ -705,7 +715,7 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
                 need = _attention_bytes(heads, c, b, window, sinks)
         wp = 0
         if need:
-            workspace = q.new_empty(need, dtype=torch.uint8)
+            workspace = _new(q, need, torch.uint8, stream)
     else:
         need = workspace.numel()
         tensors += (workspace,)

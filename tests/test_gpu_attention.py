@@ -245,6 +245,32 @@ def test_strides_streams_workspace(K):
         K.mx_cache_attention(qkv[:, ::2][:, :4], *args)
 
 
+def test_buffers_belong_to_the_calls_stream(K):
+    """What a call allocates comes from the memory of the stream it runs on:
+    the workspace is freed when the call returns, and its bytes then go to
+    that stream's next work, not to the current stream's."""
+    say("[attention buffers of a stream]")
+    rng = np.random.default_rng(24)
+    s = Setup(rng, [1, 1], [4000, 64], 4, 2, 128, 32)
+    args, q = s.args(K), s.q.cuda()
+    want = s.check(K)
+    x = torch.ones((1, 128), dtype=torch.bfloat16, device="cuda")
+    qw, sw = (torch.zeros((64, n), dtype=torch.uint8, device="cuda") for n in (64, 4))
+    need = K.mx_cache_attention_workspace(s.rows, 4, *args)
+    assert need > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = K.mx_cache_attention(q, *args, stream=side)
+    k, v = K.mx_cache_read(*args, rows=s.rows, stream=side)
+    y = K.mx_gemv(x, qw, sw, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and (y == 0).all()
+    segments = [g for g in torch.cuda.memory_snapshot() if g["stream"] == side.cuda_stream]
+    for t in (out, k, v, y):
+        assert any(0 <= t.data_ptr() - g["address"] < g["total_size"] for g in segments)
+    assert max(b["size"] for g in segments for b in g["blocks"] if b["state"] != "active_allocated") >= need
+
+
 def test_graph_decodes_a_growing_sequence(K):
     """One captured step (write, then attention) replayed while the lengths
     grow through pages and tiles; every replay equals the eager call."""
