@@ -31,10 +31,10 @@
 // and no rescaling; the sum is kept per lane and reduced once at the end.
 //
 // Few columns (attention_few_kernel): the waves of a workgroup take every
-// fourth tile and join through LDS.  Many (attention_many_kernel): every wave
-// has its own columns, and the converted tiles are shared through LDS.  Where
-// workgroups are few, long sequences are also split over them, and a second
-// kernel joins the parts.
+// fourth tile, loaded straight into LDS, and join through LDS.  Many
+// (attention_many_kernel): every wave has its own columns, and the converted
+// tiles are shared through LDS.  Both take equal shares of the batch's work,
+// which end wherever they do; a second kernel joins the parts of what was cut.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -51,7 +51,6 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;  // cache positions of a step
 constexpr int kWaves = 4;  // of a workgroup
 constexpr float kRaise = 8.0f; // log2 of how far a score may exceed the scaling maximum
-constexpr int kMaxSplits = 128;
 
 struct AttnArgs {
     const uint16_t *q;
@@ -64,12 +63,37 @@ struct AttnArgs {
     int q_heads, group;
     int window, sinks;
     float scale2; // scale * log2(e)
-    int splits;   // many columns: most splits of a sequence
-    int wanted;   // workgroups that fill the chip
-    int line;     // few columns: workgroups of a head's line (0: one for each column tile)
+    int line;     // workgroups of a head's line (0: one for each column tile)
+    int join;     // cache tiles of a workgroup that take as long as a join
     unsigned size16, magic, magic_hi; // page_size / 16; the words of floor(2^32 / size16) + 1
     int tiles;    // column tiles: an upper bound over the batch
 };
+
+// The kernel's arguments, read again from where they lie: there are more of
+// them than fit the scalar registers next to a walk through the cache, and the
+// compiler would keep what it has read.
+typedef const __attribute__((address_space(4))) AttnArgs KArgs;
+
+__device__ __forceinline__ KArgs &kernel_args()
+{
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(KArgs *)p;
+}
+
+// The lane as a value that nothing computed before depends on: what follows
+// from it is not carried in registers from one place of the work to the next.
+__device__ __forceinline__ int fresh(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+template <class A>
+__device__ __forceinline__ mx_batch batch_of(A &a)
+{
+    return {a.b.page_table, a.b.row_start, a.b.lengths, a.b.seqs, a.b.width, a.b.rows};
+}
 
 // Column tile `local` (R columns) of a sequence: its rows and positions, and
 // the cache tiles that some column sees: `sink_tiles` first ones, then
@@ -82,7 +106,8 @@ struct TilePlan {
     int sink_tiles, first_tile, n;
 };
 
-__device__ __forceinline__ TilePlan plan_tile(const AttnArgs &a, const SeqRows &seq, int local, int R)
+template <class A>
+__device__ __forceinline__ TilePlan plan_tile(A &a, const SeqRows &seq, int local, int R)
 {
     TilePlan t;
     t.seq = seq;
@@ -108,7 +133,8 @@ __device__ __forceinline__ TilePlan plan_tile(const AttnArgs &a, const SeqRows &
 }
 
 // No column tile of a sequence of this length has more cache tiles.
-__device__ __forceinline__ int most_tiles(const AttnArgs &a, int64_t len, int R)
+template <class A>
+__device__ __forceinline__ int most_tiles(A &a, int64_t len, int R)
 {
     const int64_t span = a.b.width * a.c.page_size;
     len = len < 0 ? 0 : len > span ? span : len;
@@ -131,25 +157,22 @@ struct Place {
     int64_t part;
 };
 
-// The partial results of a column tile: part i starts at row base + i stride,
-// part 0 `extra` rows later.
-struct Parts {
-    int count;
-    int64_t base, stride, extra;
-};
-
-// Column tile -> sequence and its local number: the tiles of sequence s start
-// at row_start[s] group / R + s, which leaves it at least ceil(columns / R).
-// False: the sequence has no such tile.
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int R, int tile, int lane, Place &w)
+// Column tiles are numbered so that those of sequence s start here, which
+// leaves it at least ceil(columns / R).
+__device__ __forceinline__ int64_t tiles_before(int64_t row_start, int group, int R, int s)
 {
-    auto first_of = [&](int s) {
-        const int64_t r = a.b.row_start[s];
-        return (r < 0 ? 0 : r) * a.group / R + s;
-    };
+    return (row_start < 0 ? 0 : row_start) * group / R + s;
+}
+
+// Column tile -> sequence and its local number.  False: the sequence has no
+// such tile.
+template <class A>
+__device__ __forceinline__ bool find_tile(A &a, int R, int tile, int lane, Place &w)
+{
+    auto first_of = [&](int s) { return tiles_before(a.b.row_start[s], a.group, R, s); };
     w.s = wave_search((int)a.b.seqs, tile, lane, first_of);
     const int64_t local = tile - first_of(w.s);
-    const SeqRows q = seq_rows(a.b, w.s);
+    const SeqRows q = seq_rows(batch_of(a), w.s);
     if (local < 0 || local * R >= (int64_t)q.rows * a.group)
         return false;
     w.local = (int)local;
@@ -157,96 +180,71 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int R, int tile, in
     return true;
 }
 
-// ---- many columns: a workgroup for each column tile, head and split -------
-// Cache tiles of one split: the batch's tiles over the workgroups wanted, at
-// least two per wave.  Every wave of both kernels gets the same answer.
-__device__ __forceinline__ int split_tiles(const AttnArgs &a, int R, int lane)
-{
-    float sum = 0.0f;
-    for (int s = lane; s < a.b.seqs; s += 64)
-        sum += (float)most_tiles(a, a.b.lengths[s], R);
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1)
-        sum += __shfl_xor(sum, m, 64);
-    // each sequence has about tiles / seqs column tiles for every head
-    const float units = sum * (float)a.tiles / (float)a.b.seqs * (float)a.c.heads;
-    const int per = (int)(units / (float)a.wanted) + 1;
-    return __builtin_amdgcn_readfirstlane(per < 2 * kWaves ? 2 * kWaves : per);
-}
-
-__device__ __forceinline__ Parts split_parts(const AttnArgs &a, int R, int tile, int head, int n, int lane,
-                                             int &per_split)
-{
-    Parts p{1, 0, 0, 0};
-    per_split = n;
-    if (a.splits > 1 && n > 0) {
-        const int per = split_tiles(a, R, lane);
-        const int want = (n + per - 1) / per;
-        p.count = want < a.splits ? want : a.splits;
-        per_split = (n + p.count - 1) / p.count;
-        p.count = (n + per_split - 1) / per_split;
-    }
-    p.base = ((int64_t)tile * a.c.heads + head) * R;
-    p.stride = (int64_t)a.tiles * a.c.heads * R;
-    return p;
-}
-
-// Workgroup -> (split, column tile, head), the head fastest: the eight XCDs
-// take workgroups in turn, so a head's cache stays in few L2s.  The last
-// column tiles, whose rows see most, start first.  False: nothing to do.
-__device__ __forceinline__ bool find_many(const AttnArgs &a, int R, int lane, Place &w)
-{
-    const int heads = (int)a.c.heads;
-    int id = (int)blockIdx.x;
-    w.head = id % heads;
-    id /= heads;
-    const int split = id % a.splits, tile = a.tiles - 1 - id / a.splits;
-    if (!find_tile(a, R, tile, lane, w))
-        return false;
-    int per = 0;
-    const Parts p = split_parts(a, R, tile, w.head, w.t.n, lane, per);
-    if (split >= p.count)
-        return false;
-    w.begin = split * per;
-    w.stop = w.begin + per < w.t.n ? w.begin + per : w.t.n;
-    w.part = p.count > 1 ? p.base + split * p.stride : -1;
-    return true;
-}
-
-// ---- few columns: equal shares of a line ----------------------------------
+// ---- equal shares of a line ------------------------------------------------
 // The cache tiles of all column tiles of all sequences, one after the other,
 // are cut into equal shares, one for each of a head's workgroups: a share ends
 // inside a column tile wherever it does, so lengths do not have to match for
 // the chip to be filled evenly.  A workgroup has at most one column tile that
 // began before its share and one that goes on after it, so it needs two
-// places for partial results: 2 p and 2 p + 1.  Where no sequence has more than
-// kWhole tiles, a column tile counts as one and is not cut.
+// places for partial results: 2 p and 2 p + 1.  Where the longest column tiles
+// that a workgroup gets take no longer than an equal share and a join, a
+// column tile counts as one and is not cut.  (12 ragged chunks of 16 heads:
+// 87 us, 151 with a workgroup for each column tile; 48 single tokens 117, 142;
+// eight sequences seen through a window 33, 48.)
 //
 // The arrays of the batch are read once, together, and kept in LDS.
 constexpr int kLineSeqs = 256;
-constexpr int kWhole = 12 * kWaves; // a join costs about as much as 12 tiles of a wave
+constexpr int kLineMost = 1 << 30; // places of a line: what follows is 32-bit
 
 struct LineSeq {
-    int64_t at;            // where the sequence starts in the line
-    int first, rows, len;  // its rows
+    int at;                // where the sequence starts in the line
+    int first, rows, len;  // its rows (none: where they would start)
     int per;               // tiles of one of its column tiles
 };
 
-struct Line {
-    const LineSeq *seq;
-    int64_t share, end;
-    int seqs, lane;
-    bool whole;
+// Where a workgroup is in the line.
+struct LineState {
+    int share, end; // places of a workgroup, and of the line
+    int x;          // the next place
+    int whole;      // column tiles are not cut
+};
 
-    // Every wave of the workgroup takes part; each writes the same to `to`
-    // (whole groups of 64 sequences), which is read after the barrier here.
-    __device__ __forceinline__ void build(const AttnArgs &a, int R, int lane_, LineSeq *to)
+// Sums (or maxima) of v over the lanes up to each one, v >= 0: the steps of a
+// scan along rows of 16 lanes, then across the rows.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op)
+{
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false)); // row_shr 1, 2, 4, 8
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false)); // row_bcast 15, 31
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+}
+
+// The line's sequences, in LDS after a state for each wave.
+struct Line {
+    LineState *state;
+    LineSeq *seq;
+    int lane;
+
+    __device__ __forceinline__ Line(void *lds, int lane_)
+        : state((LineState *)lds), seq((LineSeq *)(state + kWaves)), lane(lane_)
     {
-        seq = to;
-        seqs = (int)a.b.seqs;
-        lane = lane_;
+    }
+
+    // Every wave of the workgroup takes part; each writes the same (whole
+    // groups of 64 sequences), which is read after a barrier.
+    template <class A>
+    __device__ __forceinline__ LineState build(A &a, int R, int p) const
+    {
+        const auto add = [](int x, int y) { return x + y; };
+        const auto larger = [](int x, int y) { return x > y ? x : y; };
+        const int seqs = (int)a.b.seqs;
         LineSeq v[kLineSeqs / 64];
-        int most = 0;
+        int cut[kLineSeqs / 64], uncut[kLineSeqs / 64]; // up to and with the lane's sequence
+        int most = 0, places = 0, tiles = 0;            // of the longest column tile, and of all
+        int load = 0; // at least places / 1024
 #pragma unroll
         for (int k = 0; k < kLineSeqs / 64; ++k) {
             const int s = 64 * k + lane;
@@ -255,63 +253,86 @@ struct Line {
                 const int64_t b = a.b.row_start[s], e = a.b.row_start[s + 1];
                 v[k].len = a.b.lengths[s] < 0 ? 0 : a.b.lengths[s];
                 const bool ok = b >= 0 && b < e && e <= a.b.rows;
-                v[k].first = ok ? (int)b : 0;
+                v[k].first = b < 0 ? 0 : (int)b;
                 v[k].rows = ok ? (int)(e - b) : 0;
                 const int n = most_tiles(a, v[k].len, R);
                 v[k].per = n < 1 ? 1 : n;
-                most = ok && v[k].per > most ? v[k].per : most;
             }
         }
-        whole = __builtin_amdgcn_ballot_w64(most > kWhole) == 0;
-        end = 0;
 #pragma unroll
         for (int k = 0; k < kLineSeqs / 64; ++k) {
             if (64 * k >= seqs)
                 continue;
-            if (whole)
-                v[k].per = 1;
-            const int64_t all = (((int64_t)v[k].rows * a.group + R - 1) / R) * v[k].per;
-            int64_t sum = all;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const int64_t up = __shfl_up(sum, m, 64);
-                sum += lane >= m ? up : 0;
-            }
-            v[k].at = end + sum - all;
-            end += __shfl(sum, 63, 64);
-            to[64 * k + lane] = v[k];
+            const int mine = (v[k].rows * a.group + R - 1) / R;
+            const float all = (float)mine * (float)v[k].per / 1024.0f;
+            load += __builtin_amdgcn_readlane(wave_scan((int)(all < 1 << 22 ? all : 1 << 22) + 1, add), 63);
+            most = larger(most, __builtin_amdgcn_readlane(wave_scan(mine ? v[k].per : 0, larger), 63));
+            cut[k] = places + wave_scan(mine * v[k].per, add);
+            uncut[k] = tiles + wave_scan(mine, add);
+            places = __builtin_amdgcn_readlane(cut[k], 63);
+            tiles = __builtin_amdgcn_readlane(uncut[k], 63);
+            v[k].at = cut[k] - mine * v[k].per;
         }
-        end = lane64(end);
-        share = (end + a.line - 1) / a.line;
-        const int64_t least = whole ? 1 : 2 * kWaves;
+        const unsigned line = (unsigned)a.line, rounds = ((unsigned)tiles + line - 1) / line;
+        const bool whole = (float)rounds * (float)most <= (float)((unsigned)places / line + (unsigned)a.join);
+#pragma unroll
+        for (int k = 0; k < kLineSeqs / 64; ++k) {
+            if (64 * k >= seqs)
+                continue;
+            if (whole) {
+                v[k].per = 1;
+                v[k].at = uncut[k] - (v[k].rows * a.group + R - 1) / R;
+            }
+            seq[64 * k + lane] = v[k];
+        }
+        // only sequences that overlap (a row_start that decreases) have more
+        // places than a line: none of them is worked on
+        const unsigned end = load > kLineMost / 1024 ? 0u : (unsigned)(whole ? tiles : places);
+        const unsigned least = whole ? 1 : 2 * kWaves; // two tiles a wave
+        unsigned share = (end + line - 1) / line;
         share = share < least ? least : share;
-        __syncthreads();
-    }
-
-    static __device__ __forceinline__ int64_t lane64(int64_t v)
-    {
-        return (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)v) |
-                         (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+        return {(int)share, (int)end, (int)(p * share), whole};
     }
 
     // A sequence's entry, the same in all lanes.
     __device__ __forceinline__ LineSeq of(int s) const
     {
         const LineSeq v = seq[s];
-        return {lane64(v.at), __builtin_amdgcn_readfirstlane(v.first), __builtin_amdgcn_readfirstlane(v.rows),
+        return {__builtin_amdgcn_readfirstlane(v.at), __builtin_amdgcn_readfirstlane(v.first), __builtin_amdgcn_readfirstlane(v.rows),
                 __builtin_amdgcn_readfirstlane(v.len), __builtin_amdgcn_readfirstlane(v.per)};
     }
 
-    // The sequence that place x of the line belongs to: the last that starts
-    // there or before (an empty one starts where the next one does).
-    __device__ __forceinline__ int find(int64_t x) const
+    // The last sequence whose key is at most x.
+    template <class Key>
+    __device__ __forceinline__ int last(int x, int seqs, Key key) const
     {
         int n = 0;
-        for (int k = 0; 64 * k < seqs; ++k)
-            n += __popcll(__builtin_amdgcn_ballot_w64(64 * k + lane < seqs && seq[64 * k + lane].at <= x));
-        return n - 1;
+        for (int k = 0; 64 * k < seqs; ++k) {
+            const int s = 64 * k + lane;
+            n += __popcll(__builtin_amdgcn_ballot_w64(s < seqs && key(s) <= x));
+        }
+        return n > 0 ? n - 1 : 0;
+    }
+
+    // The sequence that place x of the line belongs to (an empty one starts
+    // where the next one does).
+    __device__ __forceinline__ int find(int x, int seqs) const
+    {
+        return last(x, seqs, [&](int s) { return seq[s].at; });
+    }
+
+    // The sequence that has column tile `tile`, as find_tile numbers them.
+    __device__ __forceinline__ int find_tile(int R, int group, int tile, int seqs) const
+    {
+        return last(tile, seqs, [&](int s) { return tiles_before(seq[s].first, group, R, s); });
     }
 };
+
+// Bytes of the line in LDS.
+__host__ __device__ constexpr int line_lds(int64_t seqs)
+{
+    return kWaves * (int)sizeof(LineState) + (int)((seqs + 63) / 64 * 64) * (int)sizeof(LineSeq);
+}
 
 // Largest of the four lane groups, in all of them.
 __device__ __forceinline__ float max_groups(float v)
@@ -342,32 +363,28 @@ struct Columns {
     f32x4 acc[kNQ][2 * NB];
     float m[kNQ], l[kNQ];     // scaling maximum (log2), and the lane's part of the sum
     int pos[kNQ], low[kNQ];   // the column sees [low, pos] and the first `sinks`
-    int row[kNQ], qhead[kNQ];
-    bool live[kNQ];           // not a padding column
     // positions of the wave's first and last column, and one past what it sees
     int wmin, wmax, whi;
     bool idle;                // padding columns only
 };
 
-template <int NB, int kNQ>
-__device__ __forceinline__ void load_columns(const AttnArgs &a, const Place &w, int col0, int c, int g,
+template <int NB, int kNQ, class A>
+__device__ __forceinline__ void load_columns(A &a, const Place &w, int col0, int c, int g,
                                              Columns<NB, kNQ> &q)
 {
     const TilePlan &t = w.t;
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
         const int col = col0 + n * 16 + c;
-        q.live[n] = col < t.cols;
-        const int at = q.live[n] ? col : 0, i = at / a.group;
-        q.row[n] = t.seq.first + i;
-        q.qhead[n] = w.head * a.group + at - i * a.group;
-        q.pos[n] = q.live[n] ? (int)(t.seq.pos0 + i) : -1;
-        q.low[n] = a.window && q.live[n] ? q.pos[n] - a.window + 1 : -0x7FFFFFFF;
-        const uint16_t *src = a.q + (int64_t)q.row[n] * a.q_stride + q.qhead[n] * (32 * NB) + g * (8 * NB);
+        const bool live = col < t.cols; // not a padding column
+        const int at = live ? col : 0, i = at / a.group, head = w.head * a.group + at - i * a.group;
+        q.pos[n] = live ? (int)(t.seq.pos0 + i) : -1;
+        q.low[n] = a.window && live ? q.pos[n] - a.window + 1 : -0x7FFFFFFF;
+        const uint16_t *src = a.q + (int64_t)(t.seq.first + i) * a.q_stride + head * (32 * NB) + g * (8 * NB);
 #pragma unroll
         for (int p = 0; p < NB; ++p) {
             u32x4 v = *(const u32x4 *)(src + 8 * p);
-            if (!q.live[n])
+            if (!live)
                 v = (u32x4){0, 0, 0, 0};
             q.Q[n][p] = __builtin_bit_cast(bf16x8, v);
         }
@@ -385,8 +402,8 @@ __device__ __forceinline__ void load_columns(const AttnArgs &a, const Place &w, 
 }
 
 // Does every column of the wave see all of [j0, j0 + 32)?
-template <int NB, int kNQ>
-__device__ __forceinline__ bool sees_all(const AttnArgs &a, const Columns<NB, kNQ> &q, int j0, int span)
+template <int NB, int kNQ, class A>
+__device__ __forceinline__ bool sees_all(A &a, const Columns<NB, kNQ> &q, int j0, int span)
 {
     return j0 + kTile <= q.wmin + 1 && j0 + kTile <= span && !q.idle &&
            (!a.window || j0 >= q.wmax - a.window + 1 || j0 + kTile <= a.sinks);
@@ -394,8 +411,8 @@ __device__ __forceinline__ bool sees_all(const AttnArgs &a, const Columns<NB, kN
 
 // Scores of what a column does not see become -infinity; `seen` gets the
 // positions (k slot 4h + i: position 16h + 4g + i of the tile) that it sees.
-template <int NB, int kNQ>
-__device__ __forceinline__ void mask_scores(const AttnArgs &a, const Columns<NB, kNQ> &q, int j0, int span,
+template <int NB, int kNQ, class A>
+__device__ __forceinline__ void mask_scores(A &a, const Columns<NB, kNQ> &q, int j0, int span,
                                             const bool (&there)[2], int g, f32x4 (&S)[kNQ][2], unsigned (&seen)[kNQ])
 {
 #pragma unroll
@@ -414,8 +431,8 @@ __device__ __forceinline__ void mask_scores(const AttnArgs &a, const Columns<NB,
 
 // Scores -> bf16 weights as the next product's column operand; raises the
 // running maximum (and rescales) only where a score passes it by 2^kRaise.
-template <int NB, int kNQ>
-__device__ __forceinline__ void weigh(const AttnArgs &a, Columns<NB, kNQ> &q, const f32x4 (&S)[kNQ][2],
+template <int NB, int kNQ, class A>
+__device__ __forceinline__ void weigh(A &a, Columns<NB, kNQ> &q, const f32x4 (&S)[kNQ][2],
                                       bf16x8 (&P)[kNQ])
 {
     bool raise = false;
@@ -476,14 +493,16 @@ __device__ __forceinline__ void spoil(f32x4 &acc, const f32x4 &count)
 
 // Writes the columns' results, or their parts; col0: the wave's first column in the workgroup's tile.  The lane's channels are [8 NB
 // g, 8 NB (g + 1)): channel 2 NB e + j of them is acc[j][e].
-template <int NB, int kNQ>
-__device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w, const Columns<NB, kNQ> &q, int col0,
-                                              int c, int g)
+template <int NB, int kNQ, class A>
+__device__ __forceinline__ void store_columns(A &a, const Place &w, const Columns<NB, kNQ> &q, int R,
+                                              int col0, int lane)
 {
     constexpr int dim = 32 * NB;
+    const int c = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
-        if (!q.live[n])
+        const int col = w.local * R + col0 + n * 16 + c;
+        if (col >= w.t.cols)
             continue;
         if (w.part >= 0) {
             const int64_t at = w.part + col0 + n * 16 + c;
@@ -498,7 +517,8 @@ __device__ __forceinline__ void store_columns(const AttnArgs &a, const Place &w,
                         (f32x4){q.acc[n][j][e], q.acc[n][j + 1][e], q.acc[n][j + 2][e], q.acc[n][j + 3][e]};
         } else {
             const float inv = q.l[n] == 0.0f ? 0.0f : 1.0f / q.l[n];
-            uint16_t *o = a.out + (int64_t)q.row[n] * a.out_stride + q.qhead[n] * dim + g * (8 * NB);
+            const int i = col / a.group, head = w.head * a.group + col - i * a.group;
+            uint16_t *o = a.out + (int64_t)(w.t.seq.first + i) * a.out_stride + head * dim + g * (8 * NB);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -529,7 +549,8 @@ struct Pages {
     int now, next;                            // this lane's page numbers of two windows
     int at_tile;                              // tiles taken so far
 
-    __device__ __forceinline__ Pages(const AttnArgs &a, const Place &w, int lane_, int first_, int step_, int part_)
+    template <class A>
+    __device__ __forceinline__ Pages(A &a, const Place &w, int lane_, int first_, int step_, int part_)
         : table(a.b.page_table + (int64_t)w.s * a.b.width), span(w.t.span), pages((int)a.c.pages),
           size((int)a.c.page_size), lane(lane_), size16(a.size16), magic(a.magic), magic_hi(a.magic_hi),
           sink_tiles(w.t.sink_tiles), skip(w.t.first_tile - w.t.sink_tiles), first(first_), step(step_), stop(w.stop),
@@ -757,8 +778,8 @@ __host__ __device__ constexpr int few_lds()
 }
 
 // One workgroup's cache tiles of a column tile.
-template <int NB, int kNQ, int kW, int kD>
-__device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w, int lane, int wave,
+template <int NB, int kNQ, int kW, int kD, class A>
+__device__ __forceinline__ void attention_few(A &a, const Place &w, int lane, int wave,
                                               unsigned char *lds)
 {
     using L = FewStage<NB>;
@@ -887,6 +908,8 @@ __device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w,
     // sums over the lane groups, then over the waves, through the ring (after
     // what is still in flight into it)
     __builtin_amdgcn_s_waitcnt(0x0F70u);
+    lane = fresh(lane);
+    const int col = lane & 15;
     f32x4 *so = (f32x4 *)lds;                               // [kW][kNQ][2 NB][64]
     float *sm = (float *)(so + kW * kNQ * 2 * NB * 64);     // [kW][kNQ][16], and the sums after it
     float *sl = sm + kW * kNQ * 16;
@@ -894,25 +917,25 @@ __device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w,
     for (int n = 0; n < kNQ; ++n)
         q.l[n] = sum_groups(q.l[n]);
     __syncthreads();
-    if (g == 0) {
+    if (lane < 16) {
 #pragma unroll
         for (int n = 0; n < kNQ; ++n) {
-            sm[(wave * kNQ + n) * 16 + c] = q.m[n];
-            sl[(wave * kNQ + n) * 16 + c] = q.l[n];
+            sm[(wave * kNQ + n) * 16 + col] = q.m[n];
+            sl[(wave * kNQ + n) * 16 + col] = q.l[n];
         }
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < kNQ; ++n) {
-        float up = sm[n * 16 + c];
+        float up = sm[n * 16 + col];
 #pragma unroll
         for (int x = 1; x < kW; ++x)
-            up = vmax(up, sm[(x * kNQ + n) * 16 + c]);
+            up = vmax(up, sm[(x * kNQ + n) * 16 + col]);
         float sum = 0.0f;
 #pragma unroll
         for (int x = 0; x < kW; ++x) {
-            const float mx = sm[(x * kNQ + n) * 16 + c];
-            sum += sl[(x * kNQ + n) * 16 + c] * (mx == up ? 1.0f : __builtin_amdgcn_exp2f(mx - up));
+            const float mx = sm[(x * kNQ + n) * 16 + col];
+            sum += sl[(x * kNQ + n) * 16 + col] * (mx == up ? 1.0f : __builtin_amdgcn_exp2f(mx - up));
         }
         const float f = q.m[n] == up ? 1.0f : __builtin_amdgcn_exp2f(q.m[n] - up);
         q.m[n] = up;
@@ -934,50 +957,76 @@ __device__ __forceinline__ void attention_few(const AttnArgs &a, const Place &w,
 #pragma unroll
             for (int x = 1; x < kW; ++x)
                 q.acc[n][j] += so[((x * kNQ + n) * 2 * NB + j) * 64 + lane];
-    store_columns<NB, kNQ>(a, w, q, 0, c, g);
+    store_columns<NB, kNQ>(a, w, q, R, 0, lane);
+}
+
+// Walks the places of this workgroup: `work(place)` for each, with a barrier
+// after it.  Workgroup -> (share or column tile, head), the head fastest: the
+// eight XCDs take workgroups in turn, so a head's cache stays in few L2s, and
+// the last first, whose rows see most (2048-token chunk: 598 -> 580 us).
+// `args()`: the arguments; `lds`: for the line.  kLean: nothing is kept in registers while a place is
+// worked on, which costs some 300 ns a place.
+template <bool kLean, class Args, class Work>
+__device__ __forceinline__ void for_places(Args args, int R, int lane, int wave, void *lds, Work work)
+{
+    const Line line(lds, lane);
+    LineState at{};
+    {
+        auto &a = args();
+        if (a.line) {
+            at = line.build(a, R, a.line - 1 - (int)blockIdx.x / (int)a.c.heads);
+            __syncthreads();
+        }
+    }
+    for (;;) {
+        auto &a = args();
+        const int heads = (int)a.c.heads, p = (a.line ? a.line : a.tiles) - 1 - (int)blockIdx.x / heads;
+        Place w;
+        w.head = (int)blockIdx.x % heads;
+        if (a.line) {
+            const int begin = p * at.share, end = begin + at.share < at.end ? begin + at.share : at.end;
+            if (at.x >= end)
+                return;
+            w.s = line.find(at.x, (int)a.b.seqs);
+            const LineSeq q = line.of(w.s);
+            w.local = (int)((unsigned)(at.x - q.at) / (unsigned)q.per);
+            const int tile = q.at + w.local * q.per; // the column tile's first place in the line
+            const int next = tile + q.per < end ? tile + q.per : end;
+            w.t = plan_tile(a, {q.first, q.rows, (int64_t)q.len - q.rows}, w.local, R);
+            w.begin = at.whole ? 0 : at.x - tile < w.t.n ? at.x - tile : w.t.n;
+            w.stop = at.whole ? w.t.n : next - tile < w.t.n ? next - tile : w.t.n;
+            const bool all = at.x == tile && next == tile + q.per;
+            w.part = all ? -1 : ((int64_t)(2 * p + (tile >= begin ? 1 : 0)) * heads + w.head) * R;
+            at.x = next;
+            if (kLean)
+                line.state[wave] = at;
+        } else {
+            if (!find_tile(a, R, p, lane, w))
+                return;
+            w.begin = 0;
+            w.stop = w.t.n;
+            w.part = -1;
+        }
+        work(w);
+        if (args().line == 0)
+            return;
+        __syncthreads(); // LDS is free again
+        if (kLean) {
+            at = line.state[wave];
+            at = {__builtin_amdgcn_readfirstlane(at.share), __builtin_amdgcn_readfirstlane(at.end),
+                  __builtin_amdgcn_readfirstlane(at.x), __builtin_amdgcn_readfirstlane(at.whole)};
+        }
+    }
 }
 
 template <int NB, int kNQ, int kW, int kD>
 __global__ __launch_bounds__(64 * kW, 2) void attention_few_kernel(AttnArgs a)
 {
-    constexpr int R = 16 * kNQ;
     extern __shared__ __align__(16) unsigned char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int heads = (int)a.c.heads, p = (int)blockIdx.x / heads;
-    Place w;
-    w.head = (int)blockIdx.x % heads;
-    if (a.line == 0) { // more sequences than a line holds: a column tile each
-        if (!find_tile(a, R, a.tiles - 1 - p, lane, w))
-            return;
-        w.begin = 0;
-        w.stop = w.t.n;
-        w.part = -1;
-    }
-    Line line;
-    int64_t begin = 0, end = 1;
-    if (a.line) {
-        line.build(a, R, lane, (LineSeq *)(lds + few_lds<NB, kNQ, kW, kD>()));
-        begin = p * line.share;
-        end = begin + line.share < line.end ? begin + line.share : line.end;
-    }
-    for (int64_t x = begin; x < end;) {
-        int64_t next = end;
-        if (a.line) {
-            w.s = line.find(x);
-            const LineSeq q = line.of(w.s);
-            w.local = (int)((x - q.at) / q.per);
-            const int64_t tile = q.at + (int64_t)w.local * q.per; // the column tile's first place in the line
-            next = tile + q.per < end ? tile + q.per : end;
-            w.t = plan_tile(a, {q.first, q.rows, (int64_t)q.len - q.rows}, w.local, R);
-            w.begin = line.whole ? 0 : (int)(x - tile) < w.t.n ? (int)(x - tile) : w.t.n;
-            w.stop = line.whole ? w.t.n : (int)(next - tile) < w.t.n ? (int)(next - tile) : w.t.n;
-            const bool all = x == tile && next == tile + q.per;
-            w.part = all ? -1 : ((int64_t)(2 * p + (tile >= begin ? 1 : 0)) * heads + w.head) * R;
-        }
-        attention_few<NB, kNQ, kW, kD>(a, w, lane, wave, lds);
-        x = next;
-        __syncthreads(); // the join is done with the ring
-    }
+    for_places<false>([&]() -> const AttnArgs & { return a; }, 16 * kNQ, lane, wave,
+                      lds + few_lds<NB, kNQ, kW, kD>(),
+                      [&](const Place &w) { attention_few<NB, kNQ, kW, kD>(a, w, lane, wave, lds); });
 }
 
 // Many columns: the waves have columns of their own and share the cache tiles
@@ -994,17 +1043,13 @@ struct __align__(16) WideStage {
     unsigned char nan[kWaves][64];  // per lane: the slots whose V block was NaN (stored as zeros)
 };
 
+// One workgroup's cache tiles of a column tile.
 template <int NB, int kNQ>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_many_kernel(AttnArgs a)
+__device__ __forceinline__ void attention_many(KArgs &a, const Place &w, int lane, int wave,
+                                               WideStage<NB> *stage)
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4;
     constexpr int R = 16 * kNQ * kWaves;
-    extern __shared__ __align__(16) unsigned char lds[];
-    WideStage<NB> *stage = (WideStage<NB> *)lds;
-    Place w;
-    if (!find_many(a, R, lane, w))
-        return;
+    const int c = lane & 15, g = lane >> 4;
     Columns<NB, kNQ> q;
     load_columns<NB, kNQ>(a, w, w.local * R + wave * kNQ * 16, c, g, q);
     const int end = w.t.pmax < 0 ? 0 : w.t.pmax + 1 < w.t.span ? w.t.pmax + 1 : w.t.span; // of all columns
@@ -1149,89 +1194,106 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
     for (int n = 0; n < kNQ; ++n)
         q.l[n] = sum_groups(q.l[n]);
-    store_columns<NB, kNQ>(a, w, q, wave * kNQ * 16, c, g);
+    store_columns<NB, kNQ>(kernel_args(), w, q, R, wave * kNQ * 16, fresh(lane));
 }
 
-// Joins the splits of the column tiles that have several: `per_tile`
-// workgroups of 256 threads for each column tile and head, `cols` columns at a
-// time; of the threads of a column dim / 4 lie along its channels and the rest
-// along the splits.
-template <int NB>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, int per_tile, int cols)
+// dim 64: registers for four waves a SIMD, as many as LDS holds (12 ragged
+// chunks of 16 heads: 134 -> 108 us); wider heads have LDS for two or one.
+template <int NB, int kNQ>
+__global__ __launch_bounds__(64 * kWaves)
+    __attribute__((amdgpu_waves_per_eu(NB == 2 ? 4 : 2, NB == 2 ? 4 : 2))) void attention_many_kernel(AttnArgs)
 {
-    constexpr int dim = 32 * NB, along = dim / 4;
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    WideStage<NB> *stage = (WideStage<NB> *)lds;
+    for_places<true>(kernel_args, 16 * kNQ * kWaves, lane, wave, stage + 2,
+                     [&](const Place &w) { attention_many<NB, kNQ>(kernel_args(), w, fresh(lane), wave, stage); });
+}
+
+// Joins the parts of the column tiles that have several: `per_tile` workgroups
+// of 256 threads for each column tile and head.  dim / 4 threads lie along the
+// channels of a column; the rest are columns, or, where there are many parts,
+// ways along them.  A thread loads four parts at a time, with their maxima and
+// sums, before it adds them, in order.
+template <int NB>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, int per_tile)
+{
+    constexpr int dim = 32 * NB, along = dim / 4, slots = 256 / along;
     __shared__ f32x4 so[256];
-    __shared__ float sl[256];
-    __shared__ LineSeq seqs[kLineSeqs];
+    __shared__ f32x2 sml[256];
+    __shared__ __align__(16) unsigned char lds[line_lds(kLineSeqs)];
     const int lane = threadIdx.x & 63;
-    const int part = (int)(blockIdx.x % (unsigned)per_tile);
-    const int id = (int)(blockIdx.x / (unsigned)per_tile), tile = id / (int)a.c.heads;
-    Place w;
-    w.head = id % (int)a.c.heads;
-    if (!find_tile(a, R, tile, lane, w))
+    const int chunk = (int)(blockIdx.x % (unsigned)per_tile);
+    const int id = (int)(blockIdx.x / (unsigned)per_tile), heads = (int)a.c.heads, tile = id / heads, kv = id % heads;
+    const Line line(lds, lane);
+    const LineState whole_line = line.build(a, R, 0);
+    __syncthreads();
+    const int sq = line.find_tile(R, a.group, tile, (int)a.b.seqs);
+    const LineSeq q = line.of(sq);
+    const int64_t local = tile - tiles_before(q.first, a.group, R, sq);
+    const int columns = q.rows * a.group;
+    if (whole_line.end == 0 || local < 0 || local * R >= columns)
         return;
-    Parts parts;
-    if (a.line) {
-        Line line;
-        line.build(a, R, lane, seqs);
-        const LineSeq q = line.of(w.s);
-        const int64_t start = q.at + (int64_t)w.local * q.per;
-        const int64_t p0 = start / line.share, p1 = (start + q.per - 1) / line.share;
-        parts.count = (int)(p1 - p0) + 1;
-        parts.stride = 2 * a.c.heads * R;
-        parts.extra = a.c.heads * R;
-        parts.base = (2 * p0 * a.c.heads + w.head) * R;
-    } else {
-        int per = 0;
-        parts = split_parts(a, R, tile, w.head, w.t.n, lane, per);
-    }
-    if (parts.count == 1)
+    const int first = (int)local * R, stop = first + R < columns ? first + R : columns;
+    const unsigned share = (unsigned)whole_line.share, start = (unsigned)(q.at + (int)local * q.per), p0 = start / share;
+    const int count = (int)((start + (unsigned)q.per - 1) / share - p0) + 1;
+    if (count == 1)
         return;
-    auto part_at = [&](int i) { return parts.base + i * parts.stride + (i == 0 ? parts.extra : 0); };
-    const int ways = 256 / along / cols; // threads along the splits
+    // part i starts at row base + i stride, part 0 `stride / 2` rows later
+    const int64_t stride = (int64_t)2 * heads * R, base = ((int64_t)2 * p0 * heads + kv) * R;
+    int ways = 1;
+    while (ways < slots && 4 * ways < count)
+        ways *= 2;
+    const int cols = slots / ways;
     const int d4 = threadIdx.x % along, way = threadIdx.x / along % ways, sub = threadIdx.x / along / ways;
-    const int stop = (w.local + 1) * R < w.t.cols ? (w.local + 1) * R : w.t.cols;
-    for (int col0 = w.local * R + part * cols; col0 < stop; col0 += per_tile * cols) {
+    for (int col0 = first + chunk * cols; col0 < stop; col0 += per_tile * cols) {
         const int col = col0 + sub < stop ? col0 + sub : stop - 1;
-        const int i = col / a.group, row = w.t.seq.first + i, head = w.head * a.group + col - i * a.group;
-        const int at = col - w.local * R;
+        const int64_t at = base + col - first;
         f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
         float l = 0.0f, m = -__builtin_inff();
-        for (int x = way; x < parts.count; x += ways)
-            m = vmax(m, a.part_ml[(part_at(x) + at) * 2]);
-        sl[threadIdx.x] = m;
-        __syncthreads();
-        for (int x = 0; x < ways; ++x)
-            m = vmax(m, sl[(sub * ways + x) * along + d4]);
-        __syncthreads();
-        for (int x = way; x < parts.count; x += ways) {
-            const int64_t r = part_at(x) + at;
-            const f32x2 ml = *(const f32x2 *)(a.part_ml + r * 2);
-            const float f = ml[0] == m ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - m);
-            o += f * *(const f32x4 *)(a.part_o + r * dim + d4 * 4);
-            l += f * ml[1];
-        }
-        so[threadIdx.x] = o;
-        sl[threadIdx.x] = l;
-        __syncthreads();
-        if (way == 0 && col0 + sub < stop) {
-            for (int x = 1; x < ways; ++x) {
-                o += so[threadIdx.x + x * along];
-                l += sl[threadIdx.x + x * along];
+        auto add = [&](const f32x2 &ml, const f32x4 &v) {
+            const float up = vmax(m, ml[0]);
+            const float f0 = m == up ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            const float f1 = ml[0] == up ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - up);
+            m = up;
+            o = o * f0 + v * f1;
+            l = l * f0 + ml[1] * f1;
+        };
+        for (int x = way; x < count; x += 4 * ways) {
+            f32x2 ml[4];
+            f32x4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int i = x + y * ways < count ? x + y * ways : x;
+                const int64_t r = at + i * stride + (i == 0 ? stride / 2 : 0);
+                ml[y] = *(const f32x2 *)(a.part_ml + r * 2);
+                v[y] = *(const f32x4 *)(a.part_o + r * dim + d4 * 4);
             }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (x + y * ways < count)
+                    add(ml[y], v[y]);
+        }
+        if (ways > 1) {
+            __syncthreads(); // the last columns' are read
+            so[threadIdx.x] = o;
+            sml[threadIdx.x] = (f32x2){m, l};
+            __syncthreads();
+            if (way == 0)
+                for (int x = 1; x < ways; ++x)
+                    add(sml[threadIdx.x + x * along], so[threadIdx.x + x * along]);
+        }
+        if (way == 0 && col0 + sub < stop) {
+            const int i = col / a.group, row = q.first + i, head = kv * a.group + col - i * a.group;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             *(u32x2 *)(a.out + (int64_t)row * a.out_stride + head * dim + d4 * 4) =
                 (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
         }
-        __syncthreads();
     }
 }
 
 // Stages of a wave's ring, few columns.
 constexpr int few_depth(int64_t dim) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
-
-// Bytes of the line's table in LDS.
-constexpr int line_lds(int64_t seqs) { return (int)((seqs + 63) / 64 * 64) * (int)sizeof(LineSeq); }
 
 // Workgroups of attention_few_kernel that a CU holds: by registers three with
 // one column tile (dim 64, 128), else two; by LDS as computed.
@@ -1248,9 +1310,8 @@ int few_resident(int64_t dim, int nq, int64_t seqs)
 struct Shape {
     bool many;
     int nq, R;
-    int tiles, wanted;
-    int splits; // many columns
-    int line;   // few columns
+    int tiles; // column tiles: an upper bound over the batch
+    int line, join;
     int64_t parts; // rows of partial results (0: none, and no join)
 };
 
@@ -1263,31 +1324,24 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
     s.nq = mean <= 16 || c.dim == 256 ? 1 : 2;
     s.R = 16 * s.nq * (s.many ? kWaves : 1);
     s.tiles = (int)(cols / s.R + b.seqs);
-    s.splits = 1;
-    const int64_t groups = (int64_t)s.tiles * c.heads;
     // cache tiles of the longest sequence the table can hold
     int64_t span = b.width * c.page_size;
     if (window && window + sinks + b.rows + 2 * kTile < span)
         span = window + sinks + b.rows + 2 * kTile;
-    const int64_t most = (span + kTile - 1) / kTile;
-    if (s.many) {
-        // resident workgroups, by LDS
-        s.wanted = (c.dim == 64 ? 4 : c.dim == 128 ? 2 : 1) * device_cus();
-        if (b.seqs <= kLineSeqs && 2 * groups <= s.wanted) {
-            const int64_t cut = (most + 2 * kWaves - 1) / (2 * kWaves);
-            // twice the mean: the longer sequences of a mixed batch take more
-            int64_t n = 2 * (s.wanted / groups);
-            n = n < cut ? n : cut;
-            s.splits = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
-        }
-        s.parts = s.splits > 1 ? (int64_t)s.splits * groups * s.R : 0;
-    } else {
-        s.wanted = (b.seqs <= kLineSeqs ? few_resident(c.dim, s.nq, b.seqs) : 2) * device_cus();
-        // with many column tiles the chip evens out by itself
-        if (b.seqs <= kLineSeqs && groups <= 4 * s.wanted && most > kWhole) {
-            s.line = (int)((s.wanted + c.heads - 1) / c.heads);
-            s.parts = 2 * (int64_t)s.line * c.heads * s.R;
-        }
+    const int64_t most = (span + kTile - 1) / kTile, groups = (int64_t)s.tiles * c.heads;
+    // what a join and its launch take, in tiles of a workgroup
+    s.join = s.many ? 32 : 48;
+    if (b.seqs > kLineSeqs || most <= s.join)
+        return s;
+    const int resident = !s.many         ? few_resident(c.dim, s.nq, b.seqs)
+                         : c.dim == 64   ? 4
+                         : c.dim == 128  ? 2
+                                         : 1; // by LDS
+    const int64_t fill = (int64_t)resident * device_cus();
+    // with many column tiles the chip evens out by itself
+    if (groups <= 4 * fill && s.tiles * most <= kLineMost / 2) {
+        s.line = (int)((fill + c.heads - 1) / c.heads);
+        s.parts = 2 * (int64_t)s.line * c.heads * s.R;
     }
     return s;
 }
@@ -1295,7 +1349,7 @@ Shape shape_of(int64_t q_heads, const mx_cache &c, const mx_batch &b, int64_t wi
 template <int NB, int kNQ, int kW, int kD>
 hipError_t launch_few(const AttnArgs &a, int64_t grid, hipStream_t stream)
 {
-    constexpr int most = few_lds<NB, kNQ, kW, kD>() + kLineSeqs * (int)sizeof(LineSeq);
+    constexpr int most = few_lds<NB, kNQ, kW, kD>() + line_lds(kLineSeqs);
     static_assert(most <= 160 * 1024, "LDS of a CU");
     const hipError_t e = allow_dynamic_lds((const void *)attention_few_kernel<NB, kNQ, kW, kD>, most);
     if (e != hipSuccess)
@@ -1308,18 +1362,18 @@ hipError_t launch_few(const AttnArgs &a, int64_t grid, hipStream_t stream)
 template <int NB>
 hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
 {
-    const int64_t grid = (s.line ? (int64_t)s.line : (int64_t)s.tiles * s.splits) * a.c.heads;
+    const int64_t grid = (int64_t)(s.line ? s.line : s.tiles) * a.c.heads;
     if (grid > 0x7FFFFFFF)
         return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), w(64 * kWaves);
     constexpr int kMost = NB == 8 ? 1 : 2; // column tiles a wave has registers for
     if (s.many) {
-        constexpr int bytes = 2 * (int)sizeof(WideStage<NB>);
-        const void *fn = (const void *)attention_many_kernel<NB, kMost>;
-        const hipError_t e = allow_dynamic_lds(fn, bytes);
+        constexpr int bytes = 2 * (int)sizeof(WideStage<NB>), most = bytes + line_lds(kLineSeqs);
+        static_assert(most <= 160 * 1024, "LDS of a CU");
+        const hipError_t e = allow_dynamic_lds((const void *)attention_many_kernel<NB, kMost>, most);
         if (e != hipSuccess)
             return e;
-        attention_many_kernel<NB, kMost><<<g, w, bytes, stream>>>(a);
+        attention_many_kernel<NB, kMost><<<g, w, bytes + line_lds(a.line ? a.b.seqs : 0), stream>>>(a);
     } else {
         hipError_t e;
         constexpr int kD = few_depth(32 * NB);
@@ -1331,16 +1385,11 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.parts == 0)
         return e;
-    // about 2048 workgroups (8 a CU), each with the columns abreast that leave
-    // threads for four parts or more
-    const int parts = s.line ? s.line : s.splits;
-    int cols = 256 / (8 * NB);
-    while (cols > 1 && 256 / (8 * NB) / cols < (parts < 4 ? parts : 4))
-        cols /= 2;
-    const int64_t groups = (int64_t)s.tiles * a.c.heads, chunks = (s.R + cols - 1) / cols;
+    // about 2048 workgroups (8 a CU), at most one for each column
+    const int64_t groups = (int64_t)s.tiles * a.c.heads;
     int64_t per = 2048 / groups;
-    per = per < 1 ? 1 : per > chunks ? chunks : per;
-    attention_join_kernel<NB><<<dim3((unsigned)(groups * per)), dim3(256), 0, stream>>>(a, s.R, (int)per, cols);
+    per = per < 1 ? 1 : per > s.R ? s.R : per;
+    attention_join_kernel<NB><<<dim3((unsigned)(groups * per)), dim3(256), 0, stream>>>(a, s.R, (int)per);
     return hipGetLastError();
 }
 
@@ -1370,9 +1419,8 @@ hipError_t launch_cache_attention(const uint16_t *q, int64_t q_stride, int64_t q
     a.window = (int)window;
     a.sinks = (int)sinks;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
-    a.splits = s.splits;
     a.line = s.line;
-    a.wanted = s.wanted;
+    a.join = s.join;
     a.size16 = (unsigned)(c.page_size / 16);
     const uint64_t magic = ((uint64_t)1 << 32) / a.size16 + 1;
     a.magic = (unsigned)magic;

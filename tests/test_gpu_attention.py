@@ -319,6 +319,34 @@ def test_shares_end_anywhere(K, dim, q_heads, heads):
     s.check(K, window=300, sinks=5)
 
 
+@pytest.mark.parametrize("new,q_heads", [(1, 4), (90, 2)])
+def test_row_starts_that_decrease(K, new, q_heads):
+    """A row_start that goes back and forth: its rows may count as anybody's,
+    but nothing outside the output's rows is written, and the call after it is
+    right."""
+    say(f"[attention decreasing starts] new={new}")
+    rng = np.random.default_rng(25)
+    s = Setup(rng, [new] * 9, [2000] * 9, q_heads, 1, 64, 64)
+    c, table, start, lengths = s.args(K)
+    n = s.rows
+    bad = [0, n, 0, n, n // 2, n, -5, n + 7, 0, n]
+    out = torch.full((n + 2, q_heads, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    K.mx_cache_attention(s.q.cuda(), c, table, i32(bad), lengths, out=out[1:-1])
+    torch.cuda.synchronize()
+    assert (out[0] == 9).all() and (out[-1] == 9).all()
+    s.check(K)
+
+
+@pytest.mark.parametrize("dim,lengths", [(64, [3000, 90, 1700, 400]), (128, [5000]), (256, [2600, 300])])
+def test_chunks_share_the_work(K, dim, lengths):
+    """Chunks whose column tiles are cut between workgroups."""
+    say(f"[attention chunk shares] dim={dim} lengths={lengths}")
+    rng = np.random.default_rng(26)
+    s = Setup(rng, [85, 70, 131, 129][:len(lengths)], lengths, 3, 1, dim, 112)
+    s.check(K)
+    s.check(K, window=1500, sinks=40)
+
+
 def test_more_sequences_than_a_line(K):
     # long sequences, and one more of them than the shares are made for
     say("[attention 257 sequences]")
