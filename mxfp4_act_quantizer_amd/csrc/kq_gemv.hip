@@ -246,8 +246,12 @@ __global__ __launch_bounds__(64 * kW, 2) void mx_gemv_kernel(const uint16_t *__r
 // x through LDS in chunks of kWK pairs of steps, two buffers: kWR waves with a
 // row tile each share a pair, kWK of them side by side split k.  kMT tiles of
 // 16 tokens.  A chunk lies in LDS as the products read it: piece (pair, step,
-// token tile, j) is 64 lanes x 16 bytes, the lane's slot turned by 4 j + g so
-// that the pieces of one token, written together, lie in different banks.
+// token tile, j) is 64 lanes x 16 bytes, the slots of a group permuted so that
+// the pieces of one token, written together, lie in different banks, and so do
+// the quads of two groups, read together (64 x 32768 x 8192: 70 us rotated by
+// 4 j + g, 63 so).
+__device__ __forceinline__ int turned(int c, int j, int g) { return c ^ (2 * j + (g & 1) + 8 * (g >> 1)); }
+
 template <int kMT, int kWR, int kWK, int kRing, bool kS4>
 __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const uint16_t *__restrict__ x,
                                                                           const uint8_t *__restrict__ qw,
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const 
         for (int i = 0; i < kMine; ++i) {
             const int p = t + T * i, token = p / (32 * kWK), kk = p % (32 * kWK);
             const int pu = kk / 16, gg = kk / 4 % 4, j = kk % 4;
-            to[((pu * kMT + token / 16) * 4 + j) * 64 + gg * 16 + ((token + 4 * j + gg) & 15)] = xr[i];
+            to[((pu * kMT + token / 16) * 4 + j) * 64 + gg * 16 + turned(token % 16, j, gg)] = xr[i];
         }
     };
 
@@ -322,11 +326,22 @@ __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bf16x8 w = mx_bf16x8(v.w[u][j], sc);
-                    const int slot = j * 64 + g * 16 + ((c + 4 * j + g) & 15);
+                    const int slot = j * 64 + g * 16 + turned(c, j, g);
 #pragma unroll
                     for (int a = 0; a < kMT; ++a)
                         acc[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             w, __builtin_bit_cast(bf16x8, from[(u * kMT + a) * 256 + slot]), acc[a], 0, 0, 0);
+                }
+            }
+            // LDS reads two products ahead (13 x 8960 x 2240: 8.8 -> 8.4 us;
+            // with four token tiles the order costs more than it hides)
+            if constexpr (kMT <= 2) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 2 * kMT, 0);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, kMT, 0);
+                    if (n < 6)
+                        __builtin_amdgcn_sched_group_barrier(0x100, kMT, 0);
                 }
             }
             in.load(v, 0, p + kRing * kWK);
