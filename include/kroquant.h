@@ -333,11 +333,12 @@ typedef struct mx_batch {
 /*
  * mx_cache_write: quantizes the keys and values of a step's rows into their
  * slots.  Each 32-channel block of a row is quantized as by mx_quantize_f32;
- * with `factors` the keys first go through the Kronecker transform, and get
- * the codes that kq_quantize_ex(KQ_VARIANT_BUTTERFLY) gives k as a matrix
- * [rows, heads * dim] (scores are then taken with queries transformed by the
- * transposed inverse; values need none of this online, their transform folds
- * into the projections on either side).
+ * with `factors` the keys first go through the Kronecker transform (k as a
+ * matrix [rows, heads * dim]), and get the codes of the exact transform:
+ * kq_quantize's, whose sums are fp32, but for about one code in 10^6 that lies
+ * at a rounding boundary.  (Scores are then taken with queries transformed by
+ * the transposed inverse; values need none of this online, their transform
+ * folds into the projections on either side.)
  *   k, v      dev, bf16 [rows, heads, dim], 16-byte aligned; rows are
  *             k_stride / v_stride elements apart (multiples of 8, at least
  *             heads * dim), so both may be slices of one projection's output

@@ -5,8 +5,9 @@
 // block over consecutive tokens are consecutive bytes.
 //
 // A quad of lanes holds one block of 32 channels, eight per lane, as in the
-// butterfly quantizer: the same transform stages and the same MX step, so a
-// rotated key gets exactly the codes that the butterfly kq_quantize gives it.
+// butterfly quantizer: the same transform stages and the same MX step.  A
+// rotated key gets the codes of the exact transform: where fp32 leaves a code
+// in doubt, the block is done again in double.
 //
 // A wave keeps its 16 blocks of a row (or all blocks of 16 / blocks rows, where
 // a row has fewer) and goes through up to four steps of rows with them: the
@@ -124,6 +125,114 @@ struct LanePlace {
     }
 };
 
+// ---- rotated keys: codes of the exact transform ----------------------------
+// The butterfly's five stages run in fp32, ten roundings on the way of each
+// sum, so a value may be off by gamma_10 z, z = sum_k |x_k| |K_kj| <= max|x|
+// times the product of the factors' largest column sums.  16 * 2^-24 of that
+// bound covers it and the bound's own roundings.  Where a code or the scale
+// byte would be another one within that distance (a few blocks in 10^5), the
+// wave does the block again in double, rounded to fp32 so that the conversion
+// to codes rounds as if from the double itself.  A cached key is read as often
+// as there are tokens after it, so its codes are the nearest ones: 9224 rows of
+// 8 x 128, written and read, take 34.5 us, and 31.7 without the check.
+struct Doubt {
+    float reach; // of the bound above, relative to max|x|
+
+    // f: the block's values, x: what they were computed from, of a quad.
+    __device__ __forceinline__ bool operator()(const float (&f)[8], const float (&x)[8]) const
+    {
+        float ax = 0.0f, af = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ax = amax_step(ax, x[i]);
+            af = amax_step(af, f[i]);
+        }
+        ax = vmax(ax, dpp_xor1(ax));
+        ax = vmax(ax, dpp_xor2(ax));
+        af = vmax(af, dpp_xor1(af));
+        af = vmax(af, dpp_xor2(af));
+        const float off = reach * ax;
+        const unsigned b = e8m0_byte(af - off);
+        float lo[8], hi[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = f[i] - off;
+            hi[i] = f[i] + off;
+        }
+        const float sc = scale_operand(b);
+        const bool same = b == e8m0_byte(af + off) && cvt8(lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7], sc) ==
+                                                          cvt8(hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7], sc);
+        // blocks with a NaN or an infinity are settled; where subnormals may
+        // have been rounded, or fp32 was left on the way, nothing is
+        if (!(ax < __builtin_inff()) || ax == 0.0f)
+            return false;
+        return !same || ax < 0x1p-90f || !(af + off < __builtin_inff());
+    }
+};
+
+__device__ __forceinline__ Doubt doubt_of(const float *__restrict__ F)
+{
+    float reach = 0x1p-20f;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const float c0 = __builtin_fabsf(F[4 * k]) + __builtin_fabsf(F[4 * k + 2]);
+        const float c1 = __builtin_fabsf(F[4 * k + 1]) + __builtin_fabsf(F[4 * k + 3]);
+        reach *= vmax(c0, c1);
+    }
+    return {reach};
+}
+
+__device__ __forceinline__ double dpp_double(double v, bool two)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const float lo = __uint_as_float((unsigned)b), hi = __uint_as_float((unsigned)(b >> 32));
+    const unsigned l = __float_as_uint(two ? dpp_xor2(lo) : dpp_xor1(lo));
+    const unsigned h = __float_as_uint(two ? dpp_xor2(hi) : dpp_xor1(hi));
+    return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+
+// fp32 with the last bit set where y lies between two of them (never to
+// even), so that a second rounding to fewer bits is right; not -0.
+__device__ __forceinline__ float round_to_odd(double y)
+{
+    const float r = (float)y;
+    unsigned b = __float_as_uint(r);
+    const bool finite = (b & 0x7F800000u) != 0x7F800000u;
+    if (finite && (double)r != y && !(b & 1u))
+        b += (y > (double)r) != ((b >> 31) != 0) ? 1u : 0xFFFFFFFFu;
+    return __uint_as_float(b) + 0.0f;
+}
+
+__device__ __forceinline__ void bfly_exact(float (&f)[8], const Bfly &B)
+{
+    double v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = (double)f[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fma_f64((double)B.o1, dpp_double(v[i], true), (double)B.s1 * v[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fma_f64((double)B.o2, dpp_double(v[i], false), (double)B.s2 * v[i]);
+    auto stage = [&](int st, const float(&A)[4]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & st)
+                continue;
+            const double u = v[i], w = v[i + st];
+            v[i] = fma_f64((double)A[0], u, (double)A[2] * w);
+            v[i + st] = fma_f64((double)A[1], u, (double)A[3] * w);
+        }
+    };
+    stage(4, B.a3);
+    stage(2, B.a4);
+    stage(1, B.a5);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = round_to_odd(v[i]);
+}
+
 // blockIdx.y: 0 keys, 1 values.
 template <bool kRotate>
 __global__ __launch_bounds__(64 * kWaves) void mx_cache_write_kernel(const uint16_t *__restrict__ k,
@@ -147,8 +256,12 @@ __global__ __launch_bounds__(64 * kWaves) void mx_cache_write_kernel(const uint1
             w[i] = *(const u32x4 *)(x + p.row(t, i) * stride + p.blk * 32 + qp * 8);
     p.find_slots(c, b, t, lane);
     Bfly B{};
-    if (kRotate && !value && p.lives)
-        bfly_setup(B, factors + (nT == 1 ? 0 : (int64_t)p.blk * 20), qp);
+    Doubt doubt{0.0f};
+    if (kRotate && !value && p.lives) {
+        const float *F = factors + (nT == 1 ? 0 : (int64_t)p.blk * 20);
+        bfly_setup(B, F, qp);
+        doubt = doubt_of(F);
+    }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         if (p.slot[i] < 0)
@@ -159,8 +272,19 @@ __global__ __launch_bounds__(64 * kWaves) void mx_cache_write_kernel(const uint1
             f[2 * e] = bf16lo(w[i][e]) + 0.0f; // -0 becomes +0: a code's sign means < 0
             f[2 * e + 1] = bf16hi(w[i][e]) + 0.0f;
         }
-        if (kRotate && !value)
+        if (kRotate && !value) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = f[e];
             bfly_stages(f, B);
+            if (__builtin_amdgcn_ballot_w64(doubt(f, x))) {
+                bfly_exact(x, B);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] = x[e];
+            }
+        }
         unsigned byte;
         const unsigned code = mx_encode_quad(f, byte);
         int64_t at, sat;

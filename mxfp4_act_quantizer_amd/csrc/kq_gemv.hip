@@ -422,15 +422,15 @@ hipError_t launch_mx_gemv(const uint16_t *x, int64_t M, const uint8_t *qw, const
     // x whole in LDS.  1 x 49152 x 12288: 66 us with two row tiles a wave, 72
     // with one; 1 x 12288 x 4608: 9.7 with one, 11.8 with two; 1 x 4096 x 4096:
     // 5.5 us with eight waves on k, 5.7 with four (1 x 1152 x 1152: 3.6, 3.2).
-    // 8 x 8192 x 4096: 8.9 us, in chunks 9.9; 13 x 8960 x 2240: 10.6, 8.8.
+    // 8 x 8192 x 4096: 9.0 us, in chunks 11.4; 13 x 8960 x 2240: 11.5, 8.4.
     if (M <= 8 && M * K <= kXElems) {
         if (N >= 32768)
             return launch_gemv<2, 4, 2>(a);
         return N <= 4096 && K >= 2048 ? launch_gemv<1, 8, 2>(a) : launch_gemv<1, 4, 2>(a);
     }
     // Chunks: four row tiles a workgroup where that still gives 128 of them
-    // (13 x 8960 x 2240: 8.8 us, 11.3 with two; 32 x 4096 x 4096: 15.0, 12.2),
-    // eight for many tokens and rows (64 x 32768 x 8192: 70 us, 82 with four).
+    // (13 x 8960 x 2240: 8.4 us, 10.8 with two; 32 x 4096 x 4096: 13.3, 10.6),
+    // eight for many tokens and rows (64 x 32768 x 8192: 64 us, 77 with four).
     const bool four = N / 64 >= 128;
     if (M <= 16)
         return four ? launch_gemv_chunk<1, 4, 2, 4>(a) : launch_gemv_chunk<1, 2, 4, 4>(a);

@@ -1,7 +1,8 @@
 """The paged MXFP4 cache: mx_cache_write and mx_cache_read.
 
 Codes and scales are compared bit for bit with the oracle's quantizer (plain
-rows) and with kq_quantize_ex(KQ_VARIANT_BUTTERFLY) (rotated keys); reads with
+rows), with kq_quantize_ex(KQ_VARIANT_BUTTERFLY) at a few thousand blocks
+(rotated keys) and with the transform in double at some fifty thousand; reads with
 the values that the codes stand for, exactly.  Untouched slots and rows must
 keep their bytes.  Every case prints itself before it touches the GPU."""
 import sys
@@ -125,6 +126,49 @@ def test_rotated_keys_are_the_quantizers_codes(K, heads, dim, shared):
         np.testing.assert_array_equal(got[1][page, :, :, off], s[r])
         np.testing.assert_array_equal(got[2][page, :, off], vc[r])
         np.testing.assert_array_equal(got[3][page, :, :, off], vscale[r])
+
+
+def nearest(y):
+    """MXFP4 codes and scale bytes of double blocks [..., 32]: thresholds
+    between the grid's values, a tie to the even code."""
+    amax = np.abs(y).max(-1, keepdims=True)
+    e = np.maximum(np.where(amax > 0, np.frexp(amax)[1] - 1, -200) - 2, -127)
+    v = np.abs(y) / np.ldexp(1.0, e)
+    code = sum((v > t).astype(np.uint8) for t in (0.25, 1.25, 2.5, 5.0))
+    code += sum((v >= t).astype(np.uint8) for t in (0.75, 1.75, 3.5))
+    code |= (y < 0).astype(np.uint8) << 3
+    return code[..., 0::2] | code[..., 1::2] << 4, (e[..., 0] + 127).astype(np.uint8)
+
+
+@pytest.mark.parametrize("spread", [0, 60])
+def test_rotated_keys_are_the_nearest_codes(K, spread):
+    """The transform in double and its nearest codes, 1.6 million of them, so
+    that some lie at a rounding boundary of fp32's; with `spread`, rows of very
+    small and very large values and zero rows."""
+    say(f"[cache rotated, nearest] spread={spread}")
+    rng = np.random.default_rng(31 + spread)
+    rows, heads, dim, size = 1600, 8, 128, 64
+    x = rng.standard_normal((rows, heads * dim)).astype(np.float32)
+    if spread:
+        x *= np.ldexp(np.float32(1), rng.integers(-2 * spread, spread, (rows, 1))).astype(np.float32)
+        x[::97] = 0
+    kt = torch.from_numpy(x).bfloat16()
+    f = I.random_factors(heads * dim // 32, 6)
+    cache = K.mx_cache_new(rows // size, size, heads, dim)
+    k = kt.cuda().view(rows, heads, dim)
+    K.mx_cache_write(k, k, cache, i32([range(rows // size)]), i32([0, rows]), i32([rows]), factors=dev(f))
+    y = kt.double().numpy().reshape(rows, -1, 2, 2, 2, 2, 2)
+    for axis in range(5):
+        a = f.reshape(-1, 5, 2, 2)[:, axis].astype(np.float64)
+        u = np.moveaxis(y, 2 + axis, -1)
+        u = np.stack([u[..., 0] * a[:, 0, i][:, None, None, None, None] +
+                      u[..., 1] * a[:, 1, i][:, None, None, None, None] for i in (0, 1)], -1)
+        y = np.moveaxis(u, -1, 2 + axis)
+    codes, scales = nearest(y.reshape(rows, heads, dim // 32, 32))
+    got = [b.cpu().numpy() for b in cache[:2]]
+    at = np.moveaxis(got[0], 1, 2).reshape(rows, heads, dim // 2)
+    np.testing.assert_array_equal(np.transpose(got[1], (0, 3, 1, 2)).reshape(scales.shape), scales)
+    np.testing.assert_array_equal(at, codes.reshape(at.shape))
 
 
 def test_nan_and_infinity_blocks(K):
