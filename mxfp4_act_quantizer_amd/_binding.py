@@ -494,10 +494,47 @@ def mx_cache_new(pages, page_size, heads, dim, device="cuda"):
     return MXCache(*(torch.zeros(shape, dtype=torch.uint8, device=device) for shape in (q, s, q, s)))
 
 
-# These calls are short enough on the GPU that the host side counts: the checks
-# below take the tensors' own attributes one at a time, structs are packed as
-# bytes, and the stream is the current one's raw handle rather than a new
-# Stream object.
+# These calls are short enough on the GPU that the host side counts.  The usual
+# call (the current stream, one visible GPU, tensors as documented) is checked
+# and packed by the compiled module _serving; what it returns None for is done
+# here: other streams and devices, bf16 given as bits, and every error that is
+# found before the C ABI's own checks.
+_usual = None
+_raw_stream = None
+
+
+def _serving():
+    """The compiled module, or False where it has nothing to do."""
+    global _usual, _raw_stream
+    if _usual is None:
+        torch = _torch()
+        if not torch.cuda.is_available():
+            return False
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _usual = torch.cuda.device_count() == 1 and load_serving()
+    return _usual
+
+
+def load_serving():
+    """_serving, bound to the library that is loaded (raises if it is not
+    built, or not from the library's sources)."""
+    _torch()
+    from . import _serving as module
+    if module.source_hash not in kq_build_info():
+        raise ImportError("_serving.so and libkroquant.so are not built from the same sources; build again")
+    module.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
+        "mx_gemv", "mx_cache_write", "mx_cache_read", "mx_cache_attention", "mx_cache_attention_workspace")))
+    return module
+
+
+def _done(result, where):
+    """The result of the compiled module, which returns a status for a call
+    that was refused."""
+    if type(result) is int:
+        raise KQError(result, where)
+    return result
+
+
 def _gpu(t, dtype, name):
     """Address of a contiguous GPU tensor of the dtype."""
     if t.dtype is dtype and t.is_cuda and t.is_contiguous():
@@ -603,6 +640,12 @@ def mx_gemv(x, qw, sw, out=None, out_dtype=None, stream=None):
     MXFP4 matrix W (codes [N, K/2], scales [N, K/32] u8), summed in fp32; out
     float32 (the default) or bfloat16 [M, N]."""
     torch = _torch()
+    if stream is None and (fast := _serving()):
+        dtype = out_dtype if out is None else out.dtype
+        if (dtype is None or dtype is torch.bfloat16 or dtype is torch.float32) and (out is None or out_dtype is None):
+            done = _done(fast.gemv(x, qw, sw, out, dtype is torch.bfloat16, _raw_stream(0)), "mx_gemv")
+            if done is not None:
+                return done
     M, K = _md(x)
     N = qw.shape[0]
     if qw.shape != (N, K // 2) or sw.shape != (N, K // 32):
@@ -628,6 +671,9 @@ def mx_cache_write(k, v, cache, page_table, row_start, lengths, factors=None, st
     free) of a step into their slots of the cache; `factors` [nT, 5, 2, 2]
     puts the keys through the Kronecker transform first.  Row r of sequence i
     is position lengths[i] - row_start[i + 1] + r."""
+    if stream is None and (fast := _serving()):
+        if _done(fast.write(k, v, cache, page_table, row_start, lengths, factors, _raw_stream(0)), "mx_cache_write"):
+            return
     c, heads, dim = _cache_arg(cache)
     kp, kst = _heads_view(k, "k", heads, dim)
     vp, vst = _heads_view(v, "v", heads, dim)
@@ -647,6 +693,10 @@ def mx_cache_read(cache, page_table, row_start, lengths, rows=None, k=None, v=No
     cache's codes stand for them.  `rows` sizes the outputs allocated here;
     rows of no sequence, or without a slot, are left as they were."""
     torch = _torch()
+    if stream is None and k is None and v is None and (fast := _serving()):
+        done = _done(fast.read(cache, page_table, row_start, lengths, rows, _raw_stream(0)), "mx_cache_read")
+        if done is not None:
+            return done
     c, heads, dim = _cache_arg(cache)
     if rows is None:
         if k is None:
@@ -691,6 +741,11 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
     `workspace` is a uint8 tensor of mx_cache_attention_workspace bytes
     (allocated here when not given)."""
     torch = _torch()
+    if stream is None and workspace is None and (fast := _serving()):
+        done = _done(fast.attention(q, cache, page_table, row_start, lengths, softmax_scale, window, sinks, out,
+                                    _raw_stream(0)), "mx_cache_attention")
+        if done is not None:
+            return done
     c, _, dim = _cache_arg(cache)
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, dim]")

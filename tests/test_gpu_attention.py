@@ -271,6 +271,60 @@ def test_buffers_belong_to_the_calls_stream(K):
     assert max(b["size"] for g in segments for b in g["blocks"] if b["state"] != "active_allocated") >= need
 
 
+def test_usual_calls_and_the_rest_agree(K):
+    """The compiled host side of the usual call and the Python side that takes
+    every other: the same bits, the same errors."""
+    say("[attention host sides]")
+    rng = np.random.default_rng(27)
+    s = Setup(rng, [2, 1], [700, 33], 4, 2, 64, 16)
+    args, q = s.args(K), s.q.cuda()
+    cache = args[0]
+    here = torch.cuda.current_stream()
+    want = K.mx_cache_attention(q, *args, softmax_scale=0.2, window=100, sinks=3, stream=here)
+    assert torch.equal(K.mx_cache_attention(q, *args, softmax_scale=0.2, window=100, sinks=3), want)
+    out = torch.zeros_like(q)
+    assert K.mx_cache_attention(q, *args, softmax_scale=0.2, window=100, sinks=3, out=out) is out
+    assert torch.equal(out, want)
+    bits = K.mx_cache_attention(q.view(torch.int16), *args, softmax_scale=np.float64(0.2), window=100, sinks=3)
+    assert torch.equal(bits, want)
+    plain = K.mx_cache_attention(q, *args)
+    assert torch.equal(plain, K.mx_cache_attention(q, *args, stream=here))
+    for a, b in zip(K.mx_cache_read(*args, rows=s.rows), K.mx_cache_read(*args, rows=s.rows, stream=here)):
+        assert a.dtype == torch.bfloat16 and torch.equal(a, b)
+    copies = [K.MXCache(*(t.clone() for t in cache)) for _ in range(2)]
+    kv = torch.from_numpy(rng.standard_normal((s.rows, 2, 64)).astype(np.float32)).bfloat16().cuda()
+    f = dev(I.random_factors(1, 28))
+    for c, stream in zip(copies, (None, here)):
+        assert K.mx_cache_write(kv, kv, c, *args[1:], factors=f, stream=stream) is None
+    for a, b in zip(*copies):
+        assert torch.equal(a, b)
+    x = torch.randn((3, 128), device="cuda").bfloat16()
+    w = [torch.randint(100, 130, shape, dtype=torch.uint8, device="cuda") for shape in ((40, 64), (40, 4))]
+    for dtype in (torch.float32, torch.bfloat16):
+        y = K.mx_gemv(x, *w, out_dtype=dtype)
+        assert y.dtype == dtype and torch.equal(y, K.mx_gemv(x, *w, out_dtype=dtype, stream=here))
+        z = torch.zeros_like(y)
+        assert K.mx_gemv(x, *w, out=z) is z and torch.equal(y, z)
+    assert K.mx_gemv(x, *w).dtype == torch.float32
+    for stream in (None, here):
+        for bad in (dict(softmax_scale=0.0), dict(window=-1), dict(out=q[:2]), dict(out=q)):
+            with pytest.raises((K.KQError, ValueError)):
+                K.mx_cache_attention(q, *args, stream=stream, **bad)
+        for call in (lambda: K.mx_gemv(x, w[0][:20], w[1], stream=stream),
+                     lambda: K.mx_gemv(x, *w, out_dtype=torch.float16, stream=stream),
+                     lambda: K.mx_gemv(x, *w, out=y, out_dtype=torch.float32, stream=stream),
+                     lambda: K.mx_cache_write(kv, kv[:1], cache, *args[1:], stream=stream),
+                     lambda: K.mx_cache_read(cache, args[1], args[3], args[2], rows=2, stream=stream)):
+            with pytest.raises(ValueError):
+                call()
+        for call in (lambda: K.mx_gemv(x.cpu(), *w, stream=stream), lambda: K.mx_gemv(x, w[0].int(), w[1], stream=stream),
+                     lambda: K.mx_gemv(x.float(), *w, stream=stream),
+                     lambda: K.mx_cache_write(kv.float(), kv, cache, *args[1:], stream=stream),
+                     lambda: K.mx_cache_read(cache, args[1].long(), *args[2:], rows=2, stream=stream)):
+            with pytest.raises(TypeError):
+                call()
+
+
 def test_graph_decodes_a_growing_sequence(K):
     """One captured step (write, then attention) replayed while the lengths
     grow through pages and tiles; every replay equals the eager call."""

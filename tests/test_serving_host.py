@@ -159,3 +159,24 @@ def test_binding_checks():
         K.mx_cache_new(2, 16, 2, 40, device="cpu")
     with pytest.raises(ValueError):  # buffers of two geometries
         K.mx_cache_read(c._replace(vs=c.vs[:1]), table, start, lengths, rows=3)
+
+
+def test_compiled_host_side():
+    """It is built from the library's sources, leaves what is not its call to
+    the Python side, and minds its arguments' number."""
+    torch = pytest.importorskip("torch")
+    from mxfp4_act_quantizer_amd import build as B
+    from mxfp4_act_quantizer_amd import _binding
+    fast = _binding.load_serving()
+    assert fast.source_hash == B.source_hash()
+    x, w, s = torch.zeros((1, 64)).bfloat16(), torch.zeros((8, 32), dtype=torch.uint8), torch.zeros((8, 2), dtype=torch.uint8)
+    assert fast.gemv(x, w, s, None, True, 0) is None  # tensors of the CPU
+    assert fast.gemv(1, "w", None, None, True, 0) is None
+    cache = tuple(torch.zeros(n, dtype=torch.uint8) for n in ((1, 1, 16, 32), (1, 1, 2, 16)) * 2)
+    i = torch.zeros((1, 1), dtype=torch.int32)
+    assert fast.read(cache, i, i, i, 1, 0) is None and fast.read(None, i, i, i, 1, 0) is None
+    assert fast.write(x, x, cache, i, i, i, None, 0) is None
+    assert fast.attention(x, cache, i, i, i, None, 0, 0, None, 0) is None
+    for f in (fast.gemv, fast.write, fast.read, fast.attention):
+        with pytest.raises(TypeError):
+            f(x)
