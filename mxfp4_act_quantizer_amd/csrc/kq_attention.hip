@@ -186,27 +186,33 @@ __device__ __forceinline__ bool find_tile(A &a, int R, int tile, int lane, Place
 // inside a column tile wherever it does, so lengths do not have to match for
 // the chip to be filled evenly.  A workgroup has at most one column tile that
 // began before its share and one that goes on after it, so it needs two
-// places for partial results: 2 p and 2 p + 1.  Where the longest column tiles
-// that a workgroup gets take no longer than an equal share and a join, a
-// column tile counts as one and is not cut.  (12 ragged chunks of 16 heads:
+// places for partial results: 2 p and 2 p + 1.  (12 ragged chunks of 16 heads:
 // 87 us, 151 with a workgroup for each column tile; 48 single tokens 117, 142;
-// eight sequences seen through a window 33, 48.)
+// eight sequences seen through a window 28, 48.)
+//
+// A workgroup that works on two column tiles starts twice, though, which costs
+// it about kSecond tiles.  Where cutting every column tile into pieces of its
+// own makes the longest piece no longer than that, the places of the line are
+// these pieces, one a workgroup (the window: 27.7 us, 33.3 with shares; ragged
+// chunks, whose pieces would be longer, 95.8 with pieces).  And where whole
+// column tiles take no longer than equal shares and a join, they are the pieces.
 //
 // The arrays of the batch are read once, together, and kept in LDS.
 constexpr int kLineSeqs = 256;
 constexpr int kLineMost = 1 << 30; // places of a line: what follows is 32-bit
+constexpr unsigned kSecond = 8;
 
 struct LineSeq {
     int at;                // where the sequence starts in the line
     int first, rows, len;  // its rows (none: where they would start)
-    int per;               // tiles of one of its column tiles
+    int per;               // places of one of its column tiles
 };
 
 // Where a workgroup is in the line.
 struct LineState {
     int share, end; // places of a workgroup, and of the line
     int x;          // the next place
-    int whole;      // column tiles are not cut
+    int pieces;     // a place is a piece of a column tile, not one cache tile
 };
 
 // Sums (or maxima) of v over the lanes up to each one, v >= 0: the steps of a
@@ -242,8 +248,8 @@ struct Line {
         const auto larger = [](int x, int y) { return x > y ? x : y; };
         const int seqs = (int)a.b.seqs;
         LineSeq v[kLineSeqs / 64];
-        int cut[kLineSeqs / 64], uncut[kLineSeqs / 64]; // up to and with the lane's sequence
-        int most = 0, places = 0, tiles = 0;            // of the longest column tile, and of all
+        int mine[kLineSeqs / 64];            // column tiles of the lane's sequence
+        int most = 0, places = 0, tiles = 0; // of the longest column tile, and of all; all column tiles
         int load = 0; // at least places / 1024
 #pragma unroll
         for (int k = 0; k < kLineSeqs / 64; ++k) {
@@ -263,35 +269,52 @@ struct Line {
         for (int k = 0; k < kLineSeqs / 64; ++k) {
             if (64 * k >= seqs)
                 continue;
-            const int mine = (v[k].rows * a.group + R - 1) / R;
-            const float all = (float)mine * (float)v[k].per / 1024.0f;
+            mine[k] = (v[k].rows * a.group + R - 1) / R;
+            const float all = (float)mine[k] * (float)v[k].per / 1024.0f;
             load += __builtin_amdgcn_readlane(wave_scan((int)(all < 1 << 22 ? all : 1 << 22) + 1, add), 63);
-            most = larger(most, __builtin_amdgcn_readlane(wave_scan(mine ? v[k].per : 0, larger), 63));
-            cut[k] = places + wave_scan(mine * v[k].per, add);
-            uncut[k] = tiles + wave_scan(mine, add);
-            places = __builtin_amdgcn_readlane(cut[k], 63);
-            tiles = __builtin_amdgcn_readlane(uncut[k], 63);
-            v[k].at = cut[k] - mine * v[k].per;
+            most = larger(most, __builtin_amdgcn_readlane(wave_scan(mine[k] ? v[k].per : 0, larger), 63));
+            const int upto = places + wave_scan(mine[k] * v[k].per, add);
+            v[k].at = upto - mine[k] * v[k].per;
+            places = __builtin_amdgcn_readlane(upto, 63);
+            tiles += __builtin_amdgcn_readlane(wave_scan(mine[k], add), 63);
         }
-        const unsigned line = (unsigned)a.line, rounds = ((unsigned)tiles + line - 1) / line;
-        const bool whole = (float)rounds * (float)most <= (float)((unsigned)places / line + (unsigned)a.join);
+        // a share of the line, and the least of one: two tiles a wave
+        const unsigned line = (unsigned)a.line, least = 2 * kWaves;
+        unsigned share = ((unsigned)places + line - 1) / line;
+        share = share < least ? least : share;
+        // tiles of a piece: all of a column tile, or so many that there are no
+        // more pieces than workgroups (ceil(n / each) <= n / each + 1 of each)
+        unsigned each = (unsigned)most;
+        const unsigned rounds = ((unsigned)tiles + line - 1) / line;
+        bool pieces = (float)rounds * (float)most <= (float)((unsigned)places / line + (unsigned)a.join);
+        if (!pieces && (unsigned)tiles < line) {
+            each = ((unsigned)places + line - (unsigned)tiles - 1) / (line - (unsigned)tiles);
+            each = each < least ? least : each;
+            pieces = each <= share + kSecond;
+        }
+        if (pieces) {
+            each = each < 1 ? 1 : each;
+            places = 0;
 #pragma unroll
-        for (int k = 0; k < kLineSeqs / 64; ++k) {
-            if (64 * k >= seqs)
-                continue;
-            if (whole) {
-                v[k].per = 1;
-                v[k].at = uncut[k] - (v[k].rows * a.group + R - 1) / R;
+            for (int k = 0; k < kLineSeqs / 64; ++k) {
+                if (64 * k >= seqs)
+                    continue;
+                v[k].per = (int)(((unsigned)v[k].per + each - 1) / each);
+                const int upto = places + wave_scan(mine[k] * v[k].per, add);
+                v[k].at = upto - mine[k] * v[k].per;
+                places = __builtin_amdgcn_readlane(upto, 63);
             }
-            seq[64 * k + lane] = v[k];
+            share = ((unsigned)places + line - 1) / line;
+            share = share < 1 ? 1 : share;
         }
+#pragma unroll
+        for (int k = 0; k < kLineSeqs / 64; ++k)
+            if (64 * k < seqs)
+                seq[64 * k + lane] = v[k];
         // only sequences that overlap (a row_start that decreases) have more
         // places than a line: none of them is worked on
-        const unsigned end = load > kLineMost / 1024 ? 0u : (unsigned)(whole ? tiles : places);
-        const unsigned least = whole ? 1 : 2 * kWaves; // two tiles a wave
-        unsigned share = (end + line - 1) / line;
-        share = share < least ? least : share;
-        return {(int)share, (int)end, (int)(p * share), whole};
+        const unsigned end = load > kLineMost / 1024 ? 0u : (unsigned)places;
+        return {(int)share, (int)end, (int)(p * share), pieces};
     }
 
     // A sequence's entry, the same in all lanes.
@@ -991,10 +1014,11 @@ __device__ __forceinline__ void for_places(Args args, int R, int lane, int wave,
             const LineSeq q = line.of(w.s);
             w.local = (int)((unsigned)(at.x - q.at) / (unsigned)q.per);
             const int tile = q.at + w.local * q.per; // the column tile's first place in the line
-            const int next = tile + q.per < end ? tile + q.per : end;
+            const int next = at.pieces ? at.x + 1 : tile + q.per < end ? tile + q.per : end;
             w.t = plan_tile(a, {q.first, q.rows, (int64_t)q.len - q.rows}, w.local, R);
-            w.begin = at.whole ? 0 : at.x - tile < w.t.n ? at.x - tile : w.t.n;
-            w.stop = at.whole ? w.t.n : next - tile < w.t.n ? next - tile : w.t.n;
+            const int of = at.pieces ? (int)((unsigned)(w.t.n + q.per - 1) / (unsigned)q.per) : 1; // a place's tiles
+            w.begin = (at.x - tile) * of < w.t.n ? (at.x - tile) * of : w.t.n;
+            w.stop = (next - tile) * of < w.t.n ? (next - tile) * of : w.t.n;
             const bool all = at.x == tile && next == tile + q.per;
             w.part = all ? -1 : ((int64_t)(2 * p + (tile >= begin ? 1 : 0)) * heads + w.head) * R;
             at.x = next;
@@ -1014,7 +1038,7 @@ __device__ __forceinline__ void for_places(Args args, int R, int lane, int wave,
         if (kLean) {
             at = line.state[wave];
             at = {__builtin_amdgcn_readfirstlane(at.share), __builtin_amdgcn_readfirstlane(at.end),
-                  __builtin_amdgcn_readfirstlane(at.x), __builtin_amdgcn_readfirstlane(at.whole)};
+                  __builtin_amdgcn_readfirstlane(at.x), __builtin_amdgcn_readfirstlane(at.pieces)};
         }
     }
 }
