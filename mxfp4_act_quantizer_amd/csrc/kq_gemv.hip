@@ -273,35 +273,44 @@ __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const 
     const __amdgpu_buffer_rsrc_t rx = out_buffer((void *)x, (int64_t)M * K * 2);
     const int chunks = (K + 256 * kWK - 1) / (256 * kWK);
 
-    // this thread's pieces of a chunk: token, and eight k from kk
-    u32x4 xr[kMine];
-    auto load_x = [&](int ch) {
+    // this thread's pieces of a chunk: token, and eight k from kk.  Four token
+    // tiles with four row tiles keep two chunks on the way, in an order that
+    // the compiler leaves alone (it would load them right before they are
+    // stored): 64 x 28672 x 8192 75 -> 68 us, 64 x 12288 x 4608 23.2 -> 21.4.
+    // The other forms gain nothing, or have no registers for it.
+    constexpr bool kOrdered = kMT == 4 && kWR == 4;
+    constexpr int kAhead = kOrdered ? 2 : 1;
+    static_assert(kRing % kAhead == 0, "a chunk's registers are known at compile time");
+    u32x4 xr[kAhead][kMine];
+    auto load_x = [&](int ch, u32x4 (&to)[kMine]) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int p = t + T * i, token = p / (32 * kWK), kk = p % (32 * kWK);
             const unsigned k = 256u * kWK * (unsigned)ch + 8u * (unsigned)kk;
             const unsigned drop = (unsigned)(k >= (unsigned)K) << 31;
-            xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            to[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                   rx, (int)((((unsigned)token * (unsigned)K + k) * 2u) | drop), 0, 0));
         }
     };
-    auto store_x = [&](u32x4 *to) {
+    auto store_x = [&](u32x4 *to, const u32x4 (&from)[kMine]) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int p = t + T * i, token = p / (32 * kWK), kk = p % (32 * kWK);
             const int pu = kk / 16, gg = kk / 4 % 4, j = kk % 4;
-            to[((pu * kMT + token / 16) * 4 + j) * 64 + gg * 16 + turned(token % 16, j, gg)] = xr[i];
+            to[((pu * kMT + token / 16) * 4 + j) * 64 + gg * 16 + turned(token % 16, j, gg)] = from[i];
         }
     };
 
     // this wave's pair of chunk ch is k pair ch kWK + wk
     Pair ring[kRing];
-    load_x(0);
+    load_x(0, xr[0]);
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
         in.load(ring[i], 0, i * kWK + wk);
-    store_x(xs);
-    load_x(1);
+    store_x(xs, xr[0]);
+#pragma unroll
+    for (int i = 1; i <= kAhead; ++i)
+        load_x(i, xr[i % kAhead]);
     f32x4 acc[kMT];
 #pragma unroll
     for (int a = 0; a < kMT; ++a)
@@ -314,8 +323,10 @@ __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const 
                 break;
             // this chunk is written, and every wave is done with the other buffer
             __syncthreads();
-            store_x(xs + ((ch + 1) & 1) * kPieces);
-            load_x(ch + 2); // before the codes that are loaded here: loads complete in order
+            store_x(xs + ((ch + 1) & 1) * kPieces, xr[(z + 1) % kAhead]);
+            load_x(ch + 1 + kAhead, xr[(z + 1) % kAhead]); // before the codes that are loaded here: loads complete in order
+            if constexpr (kOrdered)
+                __builtin_amdgcn_sched_barrier(0);
             const u32x4 *from = xs + (ch & 1) * kPieces + wk * (2 * kMT * 4 * 64);
             Pair &v = ring[z];
             in.exchange(v);
@@ -333,9 +344,9 @@ __global__ __launch_bounds__(64 * kWR * kWK, 2) void mx_gemv_chunk_kernel(const 
                             w, __builtin_bit_cast(bf16x8, from[(u * kMT + a) * 256 + slot]), acc[a], 0, 0, 0);
                 }
             }
-            // LDS reads two products ahead (13 x 8960 x 2240: 8.8 -> 8.4 us;
-            // with four token tiles the order costs more than it hides)
-            if constexpr (kMT <= 2) {
+            // LDS reads two products ahead (13 x 8960 x 2240: 8.8 -> 8.4 us; the
+            // other forms with four token tiles lose by it)
+            if constexpr (kMT <= 2 || kOrdered) {
                 __builtin_amdgcn_sched_group_barrier(0x100, 2 * kMT, 0);
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
