@@ -128,11 +128,13 @@ struct LanePlace {
 // ---- rotated keys: codes of the exact transform ----------------------------
 // The butterfly's five stages run in fp32, ten roundings on the way of each
 // sum, so a value may be off by gamma_10 z, z = sum_k |x_k| |K_kj| <= max|x|
-// times the product of the factors' largest column sums.  16 * 2^-24 of that
-// bound covers it and the bound's own roundings.  Where a code or the scale
-// byte would be another one within that distance (a few blocks in 10^5), the
-// wave does the block again in double, rounded to fp32 so that the conversion
-// to codes rounds as if from the double itself.  A cached key is read as often
+// times the product of the factors' largest column sums.  12 * 2^-24 of that
+// bound covers it, the rounding of value + bound and the bound's own.  Where a
+// code or the scale byte would be another one within that distance (about one
+// step of a wave in twenty), the wave does the step again in double, rounded to
+// fp32 so that the conversion to codes rounds as if from the double itself.
+// (Put off until after a wave's steps, which then need 88 registers instead of
+// 117, the second loads cost more: 39.6 us instead of 35.)  A cached key is read as often
 // as there are tokens after it, so its codes are the nearest ones: 9224 rows of
 // 8 x 128, written and read, take 34.5 us, and 31.7 without the check.
 struct Doubt {
@@ -172,7 +174,7 @@ struct Doubt {
 
 __device__ __forceinline__ Doubt doubt_of(const float *__restrict__ F)
 {
-    float reach = 0x1p-20f;
+    float reach = 0x1.8p-21f; // 12 * 2^-24
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
         const float c0 = __builtin_fabsf(F[4 * k]) + __builtin_fabsf(F[4 * k + 2]);
