@@ -746,6 +746,8 @@ def mx_cache_attention(q, cache, page_table, row_start, lengths, softmax_scale=N
                                     _raw_stream(0)), "mx_cache_attention")
         if done is not None:
             return done
+    if abs(window) >> 62 or abs(sinks) >> 62:
+        raise ValueError("window and sinks are at most 2^30")  # ctypes would cut them to 64 bits
     c, _, dim = _cache_arg(cache)
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, dim]")

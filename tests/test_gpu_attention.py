@@ -307,7 +307,8 @@ def test_usual_calls_and_the_rest_agree(K):
         assert K.mx_gemv(x, *w, out=z) is z and torch.equal(y, z)
     assert K.mx_gemv(x, *w).dtype == torch.float32
     for stream in (None, here):
-        for bad in (dict(softmax_scale=0.0), dict(window=-1), dict(out=q[:2]), dict(out=q)):
+        for bad in (dict(softmax_scale=0.0), dict(window=-1), dict(out=q[:2]), dict(out=q), dict(window=1 << 64),
+                    dict(window=7, sinks=-(1 << 70))):
             with pytest.raises((K.KQError, ValueError)):
                 K.mx_cache_attention(q, *args, stream=stream, **bad)
         for call in (lambda: K.mx_gemv(x, w[0][:20], w[1], stream=stream),
