@@ -1403,8 +1403,19 @@ hipError_t launch(const AttnArgs &a, const Shape &s, hipStream_t stream)
     } else {
         hipError_t e;
         constexpr int kD = few_depth(32 * NB);
-        e = s.nq > 1 ? launch_few<NB, kMost, kWaves, kD>(a, grid, stream)
-                     : launch_few<NB, 1, kWaves, kD>(a, grid, stream);
+        // A workgroup that has a CU to itself takes eight waves (one token over
+        // 1001, dim 128: 11.4 -> 11.0 us; 16 tokens over 1400: 14.9 -> 13.2; over
+        // 300: 7.8 -> 8.0).  Not at dim 256, where the join of eight costs more
+        // (4 tokens over 1200: 20.1 -> 21.2), nor with two column tiles a wave,
+        // which then has too few registers.
+        constexpr bool kMore = NB < 8;
+        constexpr int kLoneWaves = kMore ? 2 * kWaves : kWaves, kLoneD = kMore ? 2 : kD;
+        if (s.nq > 1)
+            e = launch_few<NB, kMost, kWaves, kD>(a, grid, stream);
+        else if (kMore && s.line == 0 && grid <= device_cus())
+            e = launch_few<NB, 1, kLoneWaves, kLoneD>(a, grid, stream);
+        else
+            e = launch_few<NB, 1, kWaves, kD>(a, grid, stream);
         if (e != hipSuccess)
             return e;
     }
